@@ -72,10 +72,12 @@ extern "C" {
 #define DFLASH_API
 #endif
 
-#define DFLASH_ABI_VERSION 2
+#define DFLASH_ABI_VERSION 3
 #define DFLASH_MAX_HEAD_DIM 512
 #define DFLASH_MAX_BLOCK_LEN 64
 #define DFLASH_MAX_SPLITS 256
+#define DFLASH_MAX_TREE_NODES 256
+#define DFLASH_MAX_TOP_K 64
 
 typedef enum dflash_status {
     DFLASH_OK = 0,
@@ -113,6 +115,8 @@ typedef enum dflash_kernel {
 #define DFLASH_DEVERR_SEQ_LEN 2u     /* seq_lens[b] < T or above the stated bounds */
 #define DFLASH_DEVERR_TIMEOUT 4u     /* a bounded pipeline wait gave up (kernel returned early) */
 #define DFLASH_DEVERR_TOKEN_ID 8u    /* a token id outside [0, vocab) (read as token 0) */
+#define DFLASH_DEVERR_TREE 16u       /* a parent outside [-1, own index), a tree size outside [0, max_nodes],
+                                        or an accepted path that is not one (tree operators) */
 
 /* Sizes and layout of one call. All counts are elements, not bytes. */
 typedef struct dflash_dims {
@@ -421,6 +425,166 @@ DFLASH_API dflash_status dflash_selector_walk(const void* pred_codebook, const v
                                               const float* uniforms, int32_t* tokens, int32_t* chosen,
                                               float* path_scores, float* q, uint32_t* device_error,
                                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Drafted trees. A drafter that proposes several tokens per position drafts a tree instead of a
+ * block: node 0 is the bonus token, every other node is a drafted token that continues its
+ * parent. Request b's tree has n_b <= max_nodes = T nodes, numbered so that a parent comes
+ * before its children; node i's row is b*T + i of every [B*T, ...] or [B, T, ...] tensor, and rows
+ * n_b .. T-1 are padding. parents[b][i] is the parent's number, or -1 for a root. num_nodes[b] =
+ * n_b (NULL: every tree has T nodes; 0: the request takes no part). The four calls below are
+ * the serving step of such a tree: score the drafter's candidates (dflash_token_logprobs),
+ * attend (dflash_tree_attn, once per layer), accept (dflash_tree_accept) and bring the accepted nodes'
+ * K/V into place (dflash_tree_commit).
+ *
+ * A parent outside [-1, i) counts as -1 and sets DFLASH_DEVERR_TREE; a tree size outside
+ * [0, T] sets DFLASH_DEVERR_TREE and the request is handled as the call says.
+ */
+
+/*
+ * Log probabilities of rows of logits: of given tokens, the entropy, and the most likely tokens.
+ * Per row with logits l_v, v in [0, vocab), and x_v = l_v / temperature:
+ *   log_z   = log(sum_v exp(x_v))
+ *   logp(v) = x_v - log_z
+ *   entropy = -sum_v exp(logp(v)) logp(v)        (a term of probability 0 is 0)
+ *   top     = the top_k tokens of largest l_v, largest first, of equal ones the smaller id first
+ * One pass over the logits: the running maximum, the sum of exponentials and the entropy's sum in
+ * fp32, the top tokens selected exactly. A logit of -inf rules its token out: logp = -inf and
+ * no share in the sums. A row of nothing but -inf has log_z = -inf, every logp = -inf and
+ * entropy 0. Logits must not be NaN or +inf (the row's results are then unspecified).
+ * The top tokens and log probabilities have the form of dflash_selector_walk's candidates and unary.
+ *
+ *   logits        device, [num_rows, vocab] of dtype (bf16 or fp32), row r at r * row_stride elements,
+ *                 row_stride >= vocab; aligned to its element size.
+ *   tokens        device int32 [num_rows, num_tokens]: the given tokens; NULL when num_tokens is 0. An
+ *                 id outside [0, vocab) gets -inf; above, it also sets DFLASH_DEVERR_TOKEN_ID
+ *                 (negative ids are padding).
+ *   token_logp    device float32 [num_rows, num_tokens], written (NULL when num_tokens is 0).
+ *   log_z, entropy  device float32 [num_rows], written, or NULL.
+ *   top_tokens    device int32 [num_rows, top_k], written (NULL when top_k is 0).
+ *   top_logp      device float32 [num_rows, top_k], written (NULL when top_k is 0).
+ *   device_error  device uint32 word (bits OR-ed in) or NULL.
+ *   workspace     device, 256-byte aligned, dflash_logprobs_workspace_bytes() long for the current
+ *                 device, zeroed once before its first use. Layout: a fixed 256 KB block of per-row
+ *                 arrival counters (left at zero by every call), then the slices' partial results.
+ * Limits: 0 <= num_rows <= 65535 (0 is a no-op), 1 <= vocab < 2^31, 0 <= num_tokens <= 64,
+ * 0 <= top_k <= min(vocab, DFLASH_MAX_TOP_K), temperature finite and >= 1e-30. Invalid arguments are
+ * reported before any launch. Asynchronous on `stream`; calls that share a workspace must not overlap.
+ */
+DFLASH_API size_t dflash_logprobs_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t top_k);
+DFLASH_API dflash_status dflash_token_logprobs(const void* logits, dflash_dtype dtype, int32_t num_rows, int32_t vocab,
+                                               int64_t row_stride, float temperature, const int32_t* tokens,
+                                               int32_t num_tokens, float* token_logp, float* log_z, float* entropy,
+                                               int32_t top_k, int32_t* top_tokens, float* top_logp,
+                                               uint32_t* device_error, void* workspace, size_t workspace_bytes,
+                                               void* stream);
+
+/*
+ * Attention of drafted trees over a paged KV cache: dflash_block_attn's layout and conventions with
+ * the tree's mask. Request b has L_b = seq_lens[b] keys: ctx_b = L_b - n_b keys of context, then
+ * its nodes' keys (node i's at position ctx_b + i of the cache). A node of depth d (roots have
+ * depth 0) stands at position p = ctx_b + d of the sequence it continues. Node i sees
+ *   context key j < ctx_b    iff window == 0 or j > p_i - window
+ *   node a's key             iff a is i or an ancestor of i, and window == 0 or p_a > p_i - window
+ * and s, out and lse are those of dflash_block_attn. A chain (parents[i] = i - 1) is
+ * dflash_block_attn with causal = 1.
+ *
+ *   q             device, [B*T, Hq, D] contiguous, dims->dtype; padding rows may hold anything.
+ *   k_cache, v_cache, page_table   as in dflash_block_attn. Keys outside [first visible, L_b) are
+ *                 never used, whatever they hold; pages without a visible key are not looked up. The
+ *                 visible keys' K and V have to be finite (a node's K and V reach the
+ *                 rows that do not see it with weight 0).
+ *   seq_lens      device, int32 [B]; n_b <= L_b <= max_seq_len.
+ *   parents       device, int32 [B, max_nodes]; num_nodes device int32 [B] or NULL.
+ *   dims          as in dflash_block_attn; max_nodes = T in [1, DFLASH_MAX_TREE_NODES].
+ *   window        0 or W >= 1; scale finite and > 0.
+ *   out           device, [B*T, Hq, D] contiguous, dims->dtype; padding rows are left as they were.
+ *   lse           device, float32 [B*T, Hq] or NULL; padding rows are left as they were.
+ *   kernel        DFLASH_KERNEL_AUTO, DFLASH_KERNEL_SIMT (CUDA cores; fp32 and every shape) or DFLASH_KERNEL_TC
+ *                 (tensor cores; bf16). AUTO takes TC for bf16 where it covers the layout (every
+ *                 page size of the contract; strides of the cache > 0).
+ *   workspace     device, 256-byte aligned, dflash_tree_attn_workspace_bytes() long for the current
+ *                 device: the error word (256 bytes, zeroed once before its first use; read with
+ *                 dflash_read_error), then the partial results of split key ranges.
+ *   wait_limit_us as in dflash_opts.
+ * A seq_len outside [n_b, max_seq_len] (DFLASH_DEVERR_SEQ_LEN) or a tree size outside [0, T]
+ * (DFLASH_DEVERR_TREE) makes the request's T rows zeros with lse = -inf. An out-of-range page id
+ * sets DFLASH_DEVERR_PAGE_ID and its keys read as zero. Invalid arguments are reported before any
+ * launch. Asynchronous on `stream`; calls that share a workspace must not overlap.
+ */
+DFLASH_API size_t dflash_tree_attn_workspace_bytes(const dflash_dims* dims, int32_t max_nodes);
+DFLASH_API dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* page_table, const int32_t* seq_lens, const int32_t* parents,
+                                          const int32_t* num_nodes, const dflash_dims* dims, int32_t max_nodes,
+                                          int32_t window, float scale, void* out, float* lse, dflash_kernel kernel,
+                                          void* workspace, size_t workspace_bytes, uint32_t wait_limit_us,
+                                          void* stream);
+
+/*
+ * Longest accepted path of drafted trees (dflash_accept_prefix for trees). With the target's token
+ * t_i = argmax_v logits[b, i, v] (the smallest id among equal maxima; logits must not be NaN) the
+ * path starts at node 0; from node i it goes on to the first child c of i (smallest number)
+ * with tokens[b, c] == t_i, and ends where there is none.
+ *   path[b, 0..a] = the path's nodes, node 0 first; path[b, a+1..T-1] = -1
+ *   accepted_len[b] = a (drafted nodes on the path)
+ *   next_token[b]   = t of the path's last node
+ *   target_argmax[b, i] = t_i, -1 in the padding, when target_argmax is not NULL
+ * A request of no nodes (n_b = 0, or a size outside [0, T]) gets accepted_len 0, path and next_token -1.
+ *
+ *   logits        device, [batch, max_nodes, vocab] of dtype (bf16 or fp32), node i of request b at
+ *                 (b * max_nodes + i) * row_stride elements; aligned to its element size. Padding rows
+ *                 are not read.
+ *   tokens        device int32 [batch, max_nodes]: the node's drafted token (node 0's is not used).
+ *   parents       device int32 [batch, max_nodes]; num_nodes device int32 [batch] or NULL.
+ *   accepted_len, next_token   device int32 [batch]; path device int32 [batch, max_nodes]; written.
+ *   target_argmax device int32 [batch, max_nodes] or NULL.
+ *   device_error  device uint32 word or NULL (DFLASH_DEVERR_TREE).
+ *   workspace     device, 256-byte aligned, dflash_tree_accept_workspace_bytes() long, zeroed once before its first use;
+ *                 the call leaves it zeroed. Layout: a fixed 512 KB block of row keys, then a fixed
+ *                 256 KB block of per-request counters, so one workspace serves calls of any size.
+ * Limits: batch >= 1, 1 <= max_nodes <= DFLASH_MAX_TREE_NODES, batch * max_nodes <= 65535,
+ * 1 <= vocab < 2^31. Invalid arguments are reported before any launch. Asynchronous on `stream`;
+ * calls that share a workspace must not overlap.
+ */
+DFLASH_API size_t dflash_tree_accept_workspace_bytes(void);
+DFLASH_API dflash_status dflash_tree_accept(const void* logits, dflash_dtype dtype, int32_t batch, int32_t max_nodes,
+                                            int32_t vocab, int64_t row_stride, const int32_t* tokens,
+                                            const int32_t* parents, const int32_t* num_nodes, int32_t* accepted_len,
+                                            int32_t* path, int32_t* next_token, int32_t* target_argmax,
+                                            uint32_t* device_error, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/*
+ * Moves the accepted nodes' K and V to consecutive cache positions, in every layer of a call:
+ *   for s = 1 .. a_b: position ctx_b + s of request b takes what position ctx_b + path[b, s] held
+ * with ctx_b = seq_lens[b] - n_b and a_b = accepted_len[b] (path and accepted_len as
+ * dflash_tree_accept writes them), and new_lens[b] = ctx_b + a_b + 1: the cache then holds
+ * the context, the bonus token and the accepted tokens. Positions past new_lens[b] keep
+ * what they held. The page table does not change.
+ *
+ *   k_cache, v_cache  device, element (layer, page, slot, head, d) at layer * layer_stride + the
+ *                 offset of dflash_block_attn's layout; dims->dtype; 16-byte aligned, strides
+ *                 multiples of 16 bytes. Written.
+ *   page_table    device int32 [B, max_pages]; seq_lens device int32 [B].
+ *   path          device int32 [B, max_nodes]; accepted_len device int32 [B].
+ *   num_nodes     device int32 [B] or NULL.
+ *   new_lens      device int32 [B], written, or NULL; may be seq_lens itself.
+ *   dims          as in dflash_block_attn (num_q_heads and max_seq_len apart: see below).
+ *   num_layers    >= 1; layer_stride elements between layers (ignored for one layer).
+ *   device_error  device uint32 word or NULL.
+ * A request is left as it is, with new_lens[b] = seq_lens[b], when n_b = 0 (not an error), when
+ * its seq_len lies outside [n_b, max_pages * page_size] (or above a non-zero dims->max_seq_len:
+ * DFLASH_DEVERR_SEQ_LEN), or when n_b is outside [0, T], accepted_len outside [0, n_b - 1] or the path not
+ * strictly increasing from 0 below n_b (DFLASH_DEVERR_TREE). A page id outside [0, num_pages) sets
+ * DFLASH_DEVERR_PAGE_ID: keys that it holds are neither read nor written. Pages that the moves
+ * touch must belong to one request only. Invalid arguments are reported before any launch.
+ * Asynchronous on `stream`; needs no workspace.
+ */
+DFLASH_API dflash_status dflash_tree_commit(void* k_cache, void* v_cache, const int32_t* page_table,
+                                            const int32_t* seq_lens, const int32_t* path, const int32_t* accepted_len,
+                                            const int32_t* num_nodes, int32_t* new_lens, const dflash_dims* dims,
+                                            int32_t max_nodes, int32_t num_layers, int64_t layer_stride,
+                                            uint32_t* device_error, void* stream);
 
 /* DFLASH_ABI_VERSION of the loaded library. */
 DFLASH_API int32_t dflash_abi_version(void);

@@ -26,7 +26,7 @@ BF16, FP32 = 0, 1
 # dflash_kernel
 KERNELS = {"auto": 0, "simt": 1, "tc": 2, "tc_pair": 3}
 # device error bits
-DEVERR_PAGE_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_TOKEN_ID = 1, 2, 4, 8
+DEVERR_PAGE_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_TOKEN_ID, DEVERR_TREE = 1, 2, 4, 8, 16
 
 EXPORTED = (
     "dflash_block_attn",
@@ -46,6 +46,13 @@ EXPORTED = (
     "dflash_grouped_conv",
     "dflash_selector_workspace_bytes",
     "dflash_selector_walk",
+    "dflash_logprobs_workspace_bytes",
+    "dflash_token_logprobs",
+    "dflash_tree_attn_workspace_bytes",
+    "dflash_tree_attn",
+    "dflash_tree_accept_workspace_bytes",
+    "dflash_tree_accept",
+    "dflash_tree_commit",
 )
 
 
@@ -147,6 +154,23 @@ def load_library(path: Optional[str] = None):
         lib.dflash_selector_walk.restype = ctypes.c_int
         lib.dflash_selector_walk.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp,
                                              vp, vp, ctypes.c_size_t, vp]
+        size, u32 = ctypes.c_size_t, ctypes.c_uint32
+        lib.dflash_logprobs_workspace_bytes.restype = size
+        lib.dflash_logprobs_workspace_bytes.argtypes = [i32, i32, i32]
+        lib.dflash_token_logprobs.restype = ctypes.c_int
+        lib.dflash_token_logprobs.argtypes = [vp, i32, i32, i32, i64, f32, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp,
+                                              size, vp]
+        lib.dflash_tree_attn_workspace_bytes.restype = size
+        lib.dflash_tree_attn_workspace_bytes.argtypes = [dims_p, i32]
+        lib.dflash_tree_attn.restype = ctypes.c_int
+        lib.dflash_tree_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, dims_p, i32, i32, f32, vp, vp, i32, vp, size, u32,
+                                         vp]
+        lib.dflash_tree_accept_workspace_bytes.restype = size
+        lib.dflash_tree_accept_workspace_bytes.argtypes = []
+        lib.dflash_tree_accept.restype = ctypes.c_int
+        lib.dflash_tree_accept.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
+        lib.dflash_tree_commit.restype = ctypes.c_int
+        lib.dflash_tree_commit.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, dims_p, i32, i32, i64, vp, vp]
         if path is None:
             _lib = lib
         return lib
@@ -553,6 +577,301 @@ def selector_walk(pred_codebook: torch.Tensor, succ_codebook: torch.Tensor, proj
                                   _stream_handle(stream))
     _check(st)
     return tokens, chosen, path_scores, q
+
+
+# ---------------------------------------------------------------------------- drafted trees
+
+
+def _stream_on(dev: torch.device, stream) -> torch.cuda.Stream:
+    """The stream of a call whose tensors are on `dev`: the given one, or dev's current stream."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if isinstance(stream, int):
+        return torch.cuda.default_stream(dev) if stream == 0 else torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream
+
+
+class _CallOn:
+    """Runs a call's allocations and launches on its stream and device, whatever the current ones are."""
+
+    def __init__(self, dev: torch.device, stream):
+        self.stream = _stream_on(dev, stream)
+        here = stream is None and torch.cuda.current_device() == dev.index
+        self.guard = None if here else torch.cuda.stream(self.stream)
+
+    def __enter__(self) -> int:
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+_tree_ws = {}
+
+
+def _tree_workspace(op: str, dev: torch.device, stream: int, nbytes: int) -> torch.Tensor:
+    """A zeroed workspace for a call without one: cached per operator, device and stream, so that calls that may
+    overlap never share one. A call that is being captured gets its own, zeroed by the graph."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    key = (op, dev.index, stream)
+    buf = _tree_ws.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        _tree_ws[key] = buf
+    return buf
+
+
+def _tree_device(**tensors) -> torch.device:
+    """The one CUDA device of the given tensors (None entries apart)."""
+    devs = {t.device for t in tensors.values() if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError(f"{', '.join(tensors)} must be on one CUDA device")
+    return next(iter(devs))
+
+
+def _expect(name: str, t: Optional[torch.Tensor], shape, dtype) -> None:
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+
+
+def _expect_error_word(t: Optional[torch.Tensor]) -> None:
+    if t is not None and (t.element_size() != 4 or t.dtype.is_floating_point or t.numel() < 1):
+        raise ValueError("device_error must hold a 32-bit integer")
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _ws_args(ws: torch.Tensor):
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def logprobs_workspace_bytes(num_rows: int, vocab: int, top_k: int) -> int:
+    """Workspace bytes of token_logprobs on the current device."""
+    n = load_library().dflash_logprobs_workspace_bytes(int(num_rows), int(vocab), int(top_k))
+    if n == 0:
+        raise DflashError(ERR_INVALID_ARG, "invalid sizes for the log probability workspace")
+    return n
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, top_k: int = 0,
+                   temperature: float = 1.0, want_entropy: bool = True, device_error: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """Log probabilities, entropy and top tokens of rows of logits (dflash_token_logprobs).
+
+    logits [..., V] bf16/fp32 whose rows have one stride (last dim contiguous); tokens int32 [..., m] (negative
+    ids are padding and get -inf). Returns (token_logp [..., m] or None, entropy [...] or None, log_z [...],
+    top_tokens int32 [..., top_k] or None, top_logp [..., top_k] or None), float32 unless said. The
+    top tokens come largest first, of equal logits the smaller id first: the candidates and unary
+    scores of selector_walk. device_error: an optional int32 device word that receives DEVERR_* bits."""
+    lib = load_library()
+    if logits.dim() < 1 or logits.shape[-1] < 1 or (logits.shape[-1] > 1 and logits.stride(-1) != 1):
+        raise ValueError("logits must be [..., V] with a contiguous last dimension")
+    lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
+    R = math.prod(lead)
+    rows = logits.reshape(R, V) if logits.is_contiguous() else logits
+    if rows.dim() != 2:
+        # leading dims of one common row stride
+        for i in range(logits.dim() - 2):
+            if logits.shape[i] > 1 and logits.stride(i) != logits.stride(i + 1) * logits.shape[i + 1]:
+                raise ValueError("the rows of logits must have one stride")
+        stride = logits.stride(-2) if logits.dim() > 1 else V
+    else:
+        stride = rows.stride(0)
+    stride = max(stride, V) if R <= 1 else stride
+    code = _dtype_code(logits)
+    m = 0
+    if tokens is not None:
+        if tokens.dim() != len(lead) + 1:
+            raise ValueError("tokens must be int32 [..., m] with the leading dims of logits")
+        m = tokens.shape[-1]
+        _expect("tokens", tokens, lead + (m,), torch.int32)
+    _expect_error_word(device_error)
+    dev = _tree_device(logits=logits, tokens=tokens, device_error=device_error, workspace=workspace)
+    with _CallOn(dev, stream) as handle:
+        f32 = dict(dtype=torch.float32, device=dev)
+        log_z = torch.empty(lead, **f32)
+        entropy = torch.empty(lead, **f32) if want_entropy else None
+        token_logp = torch.empty(lead + (m,), **f32) if tokens is not None else None
+        top_tokens = torch.empty(lead + (top_k,), dtype=torch.int32, device=dev) if top_k > 0 else None
+        top_logp = torch.empty(lead + (top_k,), **f32) if top_k > 0 else None
+        if workspace is None and R > 0:
+            workspace = _tree_workspace("token_logprobs", dev, handle, logprobs_workspace_bytes(R, V, top_k))
+        ws, ws_bytes = _ws_args(workspace) if workspace is not None else (None, 0)
+        _check(lib.dflash_token_logprobs(_ptr(logits), code, R, V, stride, float(temperature),
+                                         _ptr(tokens) if m else None, m, _ptr(token_logp) if m else None, _ptr(log_z),
+                                         _ptr(entropy), int(top_k), _ptr(top_tokens), _ptr(top_logp),
+                                         _ptr(device_error), ws, ws_bytes, handle))
+    return token_logp, entropy, log_z, top_tokens, top_logp
+
+
+def _tree_cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                     first: int) -> Dims:
+    """Dims of a cache [..., num_pages, page_size, Hkv, D] whose page dimension is `first`, and its requests."""
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride() or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must match k_cache in shape, strides and dtype")
+    if k_cache.stride(-1) != 1:
+        raise ValueError("the caches' head_dim must be contiguous")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor")
+    B = page_table.shape[0]
+    _expect("page_table", page_table, page_table.shape, torch.int32)
+    _expect("seq_lens", seq_lens, (B,), torch.int32)
+    d = Dims()
+    d.batch = B
+    d.num_q_heads = d.num_kv_heads = k_cache.shape[first + 2]
+    d.head_dim = k_cache.shape[first + 3]
+    d.page_size = k_cache.shape[first + 1]
+    d.num_pages = k_cache.shape[first]
+    d.max_pages = page_table.shape[1]
+    d.dtype = _dtype_code(k_cache)
+    d.kv_stride_page, d.kv_stride_slot, d.kv_stride_head = (int(s) for s in k_cache.stride()[first:first + 3])
+    return d
+
+
+def tree_attn_workspace_bytes(dims: Dims, max_nodes: int) -> int:
+    """Workspace bytes of tree_attn with these dims (make_dims) on the current device."""
+    lib = load_library()
+    n = lib.dflash_tree_attn_workspace_bytes(ctypes.byref(dims), int(max_nodes))
+    if n == 0:
+        raise DflashError(ERR_INVALID_ARG, lib.dflash_last_error_message().decode())
+    return n
+
+
+def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+              seq_lens: torch.Tensor, parents: torch.Tensor, num_nodes: Optional[torch.Tensor] = None, window: int = 0,
+              scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+              kernel: str = "auto", workspace: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
+              stream=None, want_lse: bool = True,
+              wait_limit_us: int = 0) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of drafted trees over a paged KV cache (dflash_tree_attn).
+
+    q [B*T, Hq, D]; k_cache, v_cache [num_pages, page_size, Hkv, D] (head_dim contiguous), the nodes' own K/V
+    among them; page_table int32 [B, max_pages]; seq_lens int32 [B] (context + nodes); parents int32
+    [B, T] (-1 for a root, else an earlier node); num_nodes int32 [B] or None (T each). Returns
+    (out [B*T, Hq, D] in q's dtype, lse fp32 [B*T, Hq] or None); padding rows of given outputs keep
+    what they held, those of new ones are zero. Without a workspace the call uses one of its stream's (or the
+    captured graph's); its error word is read with tree_attn_error()."""
+    lib = load_library()
+    if q.dim() != 3 or k_cache.dim() != 4 or parents.dim() != 2:
+        raise ValueError("q must be [B*T, Hq, D], the caches [num_pages, page_size, Hkv, D] and parents [B, T]")
+    B, T = parents.shape
+    _expect("q", q, (B * T, q.shape[1], k_cache.shape[3]), k_cache.dtype)
+    dims = _tree_cache_dims(k_cache, v_cache, page_table, seq_lens, 0)
+    dims.num_q_heads = q.shape[1]
+    dims.max_seq_len = int(max_seq_len) if max_seq_len else 0
+    _expect("seq_lens", seq_lens, (B,), torch.int32)
+    _expect("parents", parents, (B, T), torch.int32)
+    _expect("num_nodes", num_nodes, (B,), torch.int32)
+    _expect("out", out, q.shape, q.dtype)
+    _expect("lse", lse, q.shape[:2], torch.float32)
+    if kernel not in ("auto", "simt", "tc"):
+        raise ValueError("kernel must be 'auto', 'simt' or 'tc'")
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[2])
+    dev = _tree_device(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seq_lens=seq_lens,
+                       parents=parents, num_nodes=num_nodes, out=out, lse=lse, workspace=workspace)
+    with _CallOn(dev, stream) as handle:
+        fresh = torch.empty if num_nodes is None else torch.zeros
+        if workspace is None:
+            workspace = _tree_workspace("tree_attn", dev, handle, tree_attn_workspace_bytes(dims, T))
+        ws, ws_bytes = _ws_args(workspace)
+        if out is None:
+            out = fresh(q.shape, dtype=q.dtype, device=dev)
+        if lse is None and want_lse:
+            lse = fresh(q.shape[:2], dtype=torch.float32, device=dev)
+        _check(lib.dflash_tree_attn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
+                                    _ptr(parents), _ptr(num_nodes), ctypes.byref(dims), T, int(window), float(scale),
+                                    _ptr(out), _ptr(lse), KERNELS[kernel], ws, ws_bytes, int(wait_limit_us), handle))
+    return out, lse
+
+
+def tree_attn_error(device=None, stream=None, clear: bool = True) -> int:
+    """The error word (DEVERR_* bits) of the workspace that tree_attn calls without one share on a stream;
+    synchronises the stream."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    with _CallOn(dev, stream) as handle:
+        ws = _tree_ws.get(("tree_attn", dev.index, handle))
+        return 0 if ws is None else read_error(ws, clear=clear, stream=handle)
+
+
+def tree_accept(logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor,
+                num_nodes: Optional[torch.Tensor] = None, want_argmax: bool = True,
+                device_error: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """Longest accepted path of drafted trees (dflash_tree_accept): logits [B, T, V] bf16/fp32 (rows of one
+    stride, last dim contiguous), tokens and parents int32 [B, T], num_nodes int32 [B] or None. Returns
+    (accepted_len [B], path [B, T], next_token [B], target argmax [B, T] or None), int32: path holds the
+    accepted nodes from the root on, -1 behind them."""
+    lib = load_library()
+    if logits.dim() != 3 or logits.shape[2] < 1 or (logits.shape[2] > 1 and logits.stride(2) != 1):
+        raise ValueError("logits must be [B, T, V] with a contiguous last dimension")
+    B, T, V = logits.shape
+    row = logits.stride(1) if T > 1 else logits.stride(0) if B > 1 else V
+    if B > 1 and T > 1 and logits.stride(0) != T * row:
+        raise ValueError("the rows of logits must have one stride")
+    code = _dtype_code(logits)
+    _expect("tokens", tokens, (B, T), torch.int32)
+    _expect("parents", parents, (B, T), torch.int32)
+    _expect("num_nodes", num_nodes, (B,), torch.int32)
+    _expect_error_word(device_error)
+    dev = _tree_device(logits=logits, tokens=tokens, parents=parents, num_nodes=num_nodes, device_error=device_error,
+                       workspace=workspace)
+    with _CallOn(dev, stream) as handle:
+        i32 = dict(dtype=torch.int32, device=dev)
+        accepted, path, nxt = torch.empty(B, **i32), torch.empty((B, T), **i32), torch.empty(B, **i32)
+        argmax = torch.empty((B, T), **i32) if want_argmax else None
+        if workspace is None:
+            workspace = _tree_workspace("tree_accept", dev, handle, lib.dflash_tree_accept_workspace_bytes())
+        ws, ws_bytes = _ws_args(workspace)
+        _check(lib.dflash_tree_accept(_ptr(logits), code, B, T, V, row, _ptr(tokens), _ptr(parents), _ptr(num_nodes),
+                                      _ptr(accepted), _ptr(path), _ptr(nxt), _ptr(argmax), _ptr(device_error), ws,
+                                      ws_bytes, handle))
+    return accepted, path, nxt, argmax
+
+
+def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                path: torch.Tensor, accepted_len: torch.Tensor, num_nodes: Optional[torch.Tensor] = None,
+                new_lens: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
+                device_error: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Moves the accepted nodes' K/V to consecutive cache positions (dflash_tree_commit): caches
+    [num_pages, page_size, Hkv, D], or [layers, num_pages, page_size, Hkv, D] for every layer at once; path
+    int32 [B, T] and accepted_len int32 [B] of tree_accept; seq_lens int32 [B] (context + nodes).
+    Returns new_lens int32 [B] (context + bonus token + accepted tokens), which may be seq_lens itself."""
+    lib = load_library()
+    if k_cache.dim() not in (4, 5) or path.dim() != 2:
+        raise ValueError("the caches must be [(layers,) num_pages, page_size, Hkv, D] and path [B, T]")
+    first = k_cache.dim() - 4
+    dims = _tree_cache_dims(k_cache, v_cache, page_table, seq_lens, first)
+    dims.max_seq_len = int(max_seq_len) if max_seq_len else 0
+    B, T = path.shape
+    _expect("seq_lens", seq_lens, (B,), torch.int32)
+    _expect("path", path, (B, T), torch.int32)
+    _expect("accepted_len", accepted_len, (B,), torch.int32)
+    _expect("num_nodes", num_nodes, (B,), torch.int32)
+    _expect("new_lens", new_lens, (B,), torch.int32)
+    _expect_error_word(device_error)
+    dev = _tree_device(k_cache=k_cache, v_cache=v_cache, page_table=page_table, seq_lens=seq_lens, path=path,
+                       accepted_len=accepted_len, num_nodes=num_nodes, new_lens=new_lens, device_error=device_error)
+    with _CallOn(dev, stream) as handle:
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        _check(lib.dflash_tree_commit(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(path),
+                                      _ptr(accepted_len), _ptr(num_nodes), _ptr(new_lens), ctypes.byref(dims), T,
+                                      k_cache.shape[0] if first else 1, k_cache.stride(0) if first else 0,
+                                      _ptr(device_error), handle))
+    return new_lens
 
 
 def read_error(workspace: Optional[torch.Tensor] = None, clear: bool = True, stream=None) -> int:

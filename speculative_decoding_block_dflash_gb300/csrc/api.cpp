@@ -39,8 +39,11 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 size_t elem_size(int32_t dtype) { return dtype == DFLASH_BF16 ? 2 : 4; }
 
-// Validation of the sizes and layout (no pointers).
-dflash_status check_dims(const dflash_dims* d, int32_t T)
+}  // namespace
+
+// Validation of the sizes and layout (no pointers) for a block or tree of T queries, T <= max_T,
+// whose requests hold at least min_len keys.
+dflash_status check_attn_dims(const dflash_dims* d, int32_t T, int32_t max_T, int32_t min_len)
 {
     if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");
     if (d->batch < 1 || d->batch > 65535) return fail(DFLASH_ERR_INVALID_ARG, "batch %d outside [1, 65535]", d->batch);
@@ -66,10 +69,9 @@ dflash_status check_dims(const dflash_dims* d, int32_t T)
                     (long long)cap);
     if (d->dtype != DFLASH_BF16 && d->dtype != DFLASH_FP32)
         return fail(DFLASH_ERR_INVALID_ARG, "dtype %d is not DFLASH_BF16 or DFLASH_FP32", (int)d->dtype);
-    if (T < 1 || T > DFLASH_MAX_BLOCK_LEN)
-        return fail(DFLASH_ERR_INVALID_ARG, "block_len %d outside [1, %d]", T, DFLASH_MAX_BLOCK_LEN);
+    if (T < 1 || T > max_T) return fail(DFLASH_ERR_INVALID_ARG, "block_len %d outside [1, %d]", T, max_T);
     const int32_t maxL = d->max_seq_len ? d->max_seq_len : (int32_t)cap;
-    if (maxL < T) return fail(DFLASH_ERR_INVALID_ARG, "max_seq_len %d < block_len %d", maxL, T);
+    if (maxL < min_len) return fail(DFLASH_ERR_INVALID_ARG, "max_seq_len %d < block_len %d", maxL, min_len);
     const int64_t es = (int64_t)elem_size(d->dtype);
     if (d->kv_stride_page < 0 || d->kv_stride_slot < 0 || d->kv_stride_head < 0)
         return fail(DFLASH_ERR_INVALID_ARG, "negative K/V stride");
@@ -80,6 +82,10 @@ dflash_status check_dims(const dflash_dims* d, int32_t T)
                     d->head_dim);
     return DFLASH_OK;
 }
+
+namespace {
+
+dflash_status check_dims(const dflash_dims* d, int32_t T) { return check_attn_dims(d, T, DFLASH_MAX_BLOCK_LEN, T); }
 
 int32_t max_len_of(const dflash_dims* d)
 {

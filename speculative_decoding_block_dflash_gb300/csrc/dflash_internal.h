@@ -113,6 +113,9 @@ int tc_pair_row_groups(const AttnParams& p);      // pairs per (request, KV head
 cudaError_t tc_pair_grid_ctas(const AttnParams& p, int64_t* ctas);  // CTAs of the persistent launch
 cudaError_t launch_tc_pair_attn(const AttnParams& p, cudaStream_t stream);
 
+// Validation of a call's sizes and layout; reports what is wrong (csrc/api.cpp).
+dflash_status check_attn_dims(const dflash_dims* d, int32_t T, int32_t max_T, int32_t min_len);
+
 // SM count of the current device (cached per device).
 int device_sm_count();
 

@@ -1,5 +1,772 @@
-#include "tree.h"
+// Tree attention on the tensor cores (bf16): tcgen05.mma with the scores, the probabilities and the output in
+// TMEM, paged K/V staged by TMA into a shared-memory ring.
+//
+//   S [128 rows x 128 keys] = Q [128 x D] . K^T        (A: Q in shared memory, B: the K tile)
+//   O [128 rows x DV]      += P [128 x 128] . V        (A: P in TMEM, B: the V tile, MN-major)
+//
+// A query row is a (node, head of the KV head's group); a softmax thread owns a TMEM lane, that is a whole row, so the
+// row maximum and sum need no exchange between threads. P (bf16) overwrites its own S, thus costs
+// neither shared memory nor TMEM, and shared memory is left to Q and the ring: what bounds the kernel is
+// the K/V stream, whose rate is the bytes in flight over the latency.
+//
+// TMEM (512 columns): S0, S1 (128 each) and 256 columns of O. The two S buffers are used in one of three
+// ways, t counting the steps of a piece (one range's part of a request and KV head):
+//   two row tiles (DV <= 128, more than 128 rows): step t = tile t / 2, row tile t % 2, with its own O; every
+//     K/V byte serves 256 rows;
+//   one row tile, DV <= 128: step t = tile t, its O the one of t % 2: two warpgroups take alternate tiles
+//     with a maximum, a sum and an O each, joined when the piece ends, so neither waits for the other;
+//   one row tile, DV = 256: step t = tile t, one O, one warpgroup; S(t+1) is computed while the
+//     softmax of S(t) runs. For head_dim above 256 a CTA computes 256 of the output's dims from the whole S.
+// In all three the MMA warp does: S(0), S(1), then for every t: O += P(t) V, S(t + 2), which reuses
+// the buffer of P(t) (MMAs of one thread execute in order).
+//
+// Online softmax about a lazy maximum: a row's maximum moves only when a score exceeds it by 2^8 in the exp2 domain; O
+// and the sum are then rescaled in place. P <= 2^8 in bf16 rounds each probability to 2^-8 relative, the same choice the
+// block attention makes: the products with V average such errors out, and P in fp32 would need tf32
+// MMAs of a quarter of the rate. The row sums add the unrounded probabilities in fp32.
+//
+// Masks are only looked at in tiles that hold tree keys or a window's edge: a node's visible keys of 32 positions are
+// one word, made from its ancestors' bits. V rows that no node sees are zeroed in shared memory, as 0 x NaN would
+// reach every row.
+//
+// Warps: 0-3 and 4-7 softmax and output, 8-10 TMA producers, 11 the MMA issuer. Ring stages are 16 KB: K 128 keys
+// x 64 dims; V 64 keys x 128 dims (128 keys x 64 dims at DV = 64). A box is 64 dims of up to 64 tokens of
+// one page; its id is read one stage ahead by the lane that issues it. Boxes past the keys or before the window are
+// fetched at an out-of-bounds page, which the TMA unit fills with zeros without a look at the table.
+//
+// Every mbarrier wait is bounded (p.wait_ns): on expiry the kernel records DFLASH_DEVERR_TIMEOUT, waits (bounded) for its
+// own copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "tc_ptx.cuh"
+#include "tree_attn.cuh"
+
 namespace dflash {
-bool tree_tc_supports(const dflash_dims*) { return false; }
-cudaError_t launch_tree_attn_tc(const TreeAttnParams&, cudaStream_t) { return cudaErrorNotSupported; }
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8;
+constexpr int kProducers = 3;
+constexpr int kMmaWarp = 11;
+constexpr int kTile = 128;
+constexpr int kStageBytes = 16384;
+constexpr int kMaxStages = 13;
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kOCol = 256;  // first TMEM column of O
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThresh = 8.0f;
+
+struct TcShape {
+    int32_t stages;   // ring depth
+    int32_t q_rows;   // rows of Q in shared memory (p.rows rounded up to 8)
+    int32_t box;      // tokens per box
+};
+
+// Shared memory after the alignment gap: Q, the ring, then this.
+struct TcMisc {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full, q_free;
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t abort;
+    float m[2][128], l[2][128];
+    int32_t par[DFLASH_MAX_TREE_NODES];
+    // then lo [npt], ancestor words [npt][(T + 31) / 32]
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Loads 32 columns and waits; later uses of the registers are ordered after the wait.
+__device__ __forceinline__ void load32(uint32_t taddr, uint32_t (&r)[32])
+{
+    tmem_ld32(taddr, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// D (TMEM) (+)= A (TMEM, bf16 pairs) . B (shared memory)
+__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
+        : "memory");
+}
+
+// A ring position that advances by `by` stages.
+struct RingPos {
+    int32_t idx;
+    uint32_t phase;
+    __device__ __forceinline__ void advance(int by, int stages)
+    {
+        idx += by;
+        if (idx >= stages) {
+            idx -= stages;
+            phase ^= 1u;
+        }
+    }
+};
+
+// What ring stage i of a piece of n tiles holds. One row tile: K0 K1 V0 K2 V1 ... V(n-1); two: K0 V0 K1 V1 ...
+struct StageOf {
+    bool is_k;
+    int32_t tile, sub;
+};
+
+__device__ __forceinline__ StageOf stage_of(int32_t i, int32_t n, bool two, int32_t kc, int32_t vs)
+{
+    StageOf s;
+    if (two) {
+        const int32_t j = i / (kc + vs), r = i - j * (kc + vs);
+        s.is_k = r < kc;
+        s.tile = j;
+        s.sub = s.is_k ? r : r - kc;
+        return s;
+    }
+    if (i < kc) return StageOf{true, 0, i};
+    const int32_t j = (i - kc) / (kc + vs), r = i - kc - j * (kc + vs);
+    s.is_k = j < n - 1 && r < kc;
+    s.tile = s.is_k ? j + 1 : j;
+    s.sub = s.is_k || j == n - 1 ? r : r - kc;
+    return s;
+}
+
+// Bits a .. b - 1 of a word (a and b outside [0, 32] are taken to its ends).
+__device__ __forceinline__ uint32_t bit_span(int32_t a, int32_t b)
+{
+    a = max(a, 0);
+    b = min(b, 32);
+    if (b <= a) return 0u;
+    return (b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+template <int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const TreeAttnParams p, const TcShape x)
+{
+    constexpr bool kAlternate = DV <= 128;        // two O accumulators
+    constexpr int kVN = DV == 64 ? 64 : 128;      // dims of a V stage
+    constexpr int kVKeys = DV == 64 ? 128 : 64;   // and its keys
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int32_t kc_n = (p.D + 63) / 64;
+    uint8_t* q_s = smem;
+    uint8_t* ring = smem + (size_t)kc_n * x.q_rows * 128;
+    TcMisc& ms = *reinterpret_cast<TcMisc*>(ring + (size_t)x.stages * kStageBytes);
+    int32_t* lo_s = reinterpret_cast<int32_t*>(&ms + 1);
+    uint32_t* anc_s = reinterpret_cast<uint32_t*>(lo_s + p.npt);
+    volatile int* abort_flag = &ms.abort;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t range = blockIdx.x / p.n_sub, sub = blockIdx.x % p.n_sub;
+    const SubTile st = sub_tile(p, sub);
+    const int32_t node0 = st.rt * p.npt;
+    const int32_t vc_n = (min(DV, p.D - st.dv * DV) + kVN - 1) / kVN;  // V column groups
+    const int32_t vs_n = (kTile / kVKeys) * vc_n;                       // V stages per tile
+    const int S = x.stages;
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(ms.full + i, 1);
+            mbar_init(ms.empty + i, 1);
+        }
+        mbar_init(&ms.q_full, 1);
+        mbar_init(&ms.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(ms.s_full + i, 1);
+            mbar_init(ms.p_full + i, 128);
+            mbar_init(ms.o_done + i, 1);
+        }
+        mbar_init(&ms.drain, 1);
+        ms.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ms.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cudaTriggerProgrammaticLaunchCompletion();  // the join grid may take its place; it waits for this one to end
+    const uint32_t tmem = ms.tmem;
+
+    PieceWalk w;
+    w.start(p, range);
+    bool ok = true;
+    auto live_rows = [&]() -> int32_t { return min(p.npt, w.req.n - node0) * p.Gc; };  // <= 0: nothing for this CTA
+
+    if (warp >= kProducerWarp && warp < kProducerWarp + kProducers) {
+        // ------------------------------------------------------------------ TMA producers
+        const int pw = warp - kProducerWarp;
+        const uint64_t kv_policy = l2_policy_evict_first();
+        const int32_t boxes = kTile / x.box;                 // per stage, K and V alike
+        RingPos pos{pw, 0u};
+        uint32_t issued = 0, issued_phase = 0, q_phase = 0;
+        bool q_out = false;
+        int32_t skew = pw;  // this warp's next stage of the piece: every third one, counted across pieces
+        for (; !w.done() && ok; w.next(p)) {
+            const int32_t live = live_rows();
+            if (live <= 0) continue;
+            const bool two = kAlternate && live > 128;
+            const int32_t n = w.t1 - w.t0;
+            const int32_t total = n * (kc_n + vs_n);
+            if (pw == 0) {
+                // Q once the last piece's scores are computed
+                if (lane == 0) {
+                    ok = ring_wait(&ms.q_free, q_phase ^ 1u, abort_flag, p.err, p.wait_ns);
+                    if (ok) {
+                        mbar_expect_tx(&ms.q_full, (uint32_t)(kc_n * p.rows * 128));
+                        for (int kc = 0; kc < kc_n; ++kc)
+                            tma_load_3d(q_s + (size_t)kc * x.q_rows * 128, &tm_q, &ms.q_full, kc * 64,
+                                        w.g * p.G + st.gc * p.Gc, w.b * p.T + node0);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                q_phase ^= 1u;
+                q_out = true;
+            }
+            // this lane's box of stage i: page id and coordinates
+            struct Box {
+                int32_t page, slot, dim, dst;
+            };
+            auto box_of = [&](int32_t i) -> Box {
+                Box bx{p.num_pages, 0, 0, 0};
+                if (lane >= boxes) return bx;
+                const StageOf so = stage_of(i, n, two, kc_n, vs_n);
+                int32_t key = (w.req.tile0 + w.t0 + so.tile) * kTile;
+                if (so.is_k) {
+                    key += lane * x.box;
+                    bx.dim = so.sub * 64;
+                    bx.dst = lane * x.box * 128;
+                } else if (DV == 64) {
+                    key += lane * x.box;
+                    bx.dim = 0;
+                    bx.dst = lane * x.box * 128;
+                } else {
+                    const int32_t per = boxes / 2, h = so.sub / vc_n, c = so.sub - h * vc_n;
+                    const int32_t slab = lane / per, i2 = lane - slab * per;
+                    key += h * 64 + i2 * x.box;
+                    bx.dim = st.dv * DV + c * 128 + slab * 64;
+                    bx.dst = slab * 8192 + i2 * x.box * 128;
+                }
+                if (key < w.req.L && key + x.box > w.req.lo) {
+                    const int32_t pg = key / p.page_size;
+                    bx.slot = key - pg * p.page_size;
+                    const int32_t id = __ldg(p.page_table + (int64_t)w.b * p.max_pages + pg);
+                    if (id >= 0 && id < p.num_pages)
+                        bx.page = id;
+                    else
+                        raise_error(p.err, DFLASH_DEVERR_PAGE_ID);
+                }
+                return bx;
+            };
+            int32_t i = skew;
+            Box cur{p.num_pages, 0, 0, 0};
+            if (i < total) cur = box_of(i);
+#pragma unroll 1
+            for (; i < total; i += kProducers) {
+                Box nxt{p.num_pages, 0, 0, 0};
+                if (i + kProducers < total) nxt = box_of(i + kProducers);
+                if (lane == 0) {
+                    ok = ring_wait(ms.empty + pos.idx, pos.phase ^ 1u, abort_flag, p.err, p.wait_ns);
+                    if (ok) mbar_expect_tx(ms.full + pos.idx, kStageBytes);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (lane < boxes) {
+                    const CUtensorMap* map = stage_of(i, n, two, kc_n, vs_n).is_k ? &tm_k : &tm_v;
+                    uint8_t* dst = ring + (size_t)pos.idx * kStageBytes + cur.dst;
+                    // read once: the first to leave L2, unless other query tiles read it again
+                    if (p.n_sub == 1)
+                        tma_load_4d_hint(dst, map, ms.full + pos.idx, cur.dim, w.g, cur.slot, cur.page, kv_policy);
+                    else
+                        tma_load_4d(dst, map, ms.full + pos.idx, cur.dim, w.g, cur.slot, cur.page);
+                }
+                __syncwarp();
+                issued |= 1u << pos.idx;
+                issued_phase = (issued_phase & ~(1u << pos.idx)) | (pos.phase << pos.idx);
+                pos.advance(kProducers, S);
+                cur = nxt;
+            }
+            skew = i - total;
+        }
+        // no copy of ours may land after the CTA has gone
+        if (!ok && lane == 0) {
+            const unsigned long long t0 = globaltimer();
+            for (int s = 0; s < S; ++s)
+                if (issued & (1u << s))
+                    while (!mbar_test_wait(ms.full + s, (issued_phase >> s) & 1u) && globaltimer() - t0 < p.wait_ns) {
+                    }
+            if (q_out)
+                while (!mbar_test_wait(&ms.q_full, q_phase ^ 1u) && globaltimer() - t0 < p.wait_ns) {
+                }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc_s = make_idesc(128, kTile, 0, 0);
+        constexpr uint32_t idesc_o = make_idesc(128, kVN, 0, 1);
+        const uint32_t q_addr = smem_u32(q_s), ring_addr = smem_u32(ring);
+        RingPos pos{0, 0u};
+        uint32_t q_phase = 0, p_phase = 0;  // p_phase: bit b = parity of the next P in buffer b
+        auto wait0 = [&](uint64_t* bar, uint32_t parity) -> bool {
+            bool got = true;
+            if (lane == 0) got = ring_wait(bar, parity, abort_flag, p.err, p.wait_ns);
+            got = __shfl_sync(0xffffffffu, got, 0);
+            tc_fence_after();
+            return got;
+        };
+        for (; !w.done() && ok; w.next(p)) {
+            const int32_t live = live_rows();
+            if (live <= 0) continue;
+            const bool two = kAlternate && live > 128;
+            const int32_t n = w.t1 - w.t0, steps = two ? 2 * n : n;
+            ok = wait0(&ms.q_full, q_phase);
+            if (!ok) break;
+            q_phase ^= 1u;
+            // S(t) = Q K^T. `fresh`: the first use of the tile's stages (they are waited for); `last`: the
+            // last (they are released). Otherwise the stages stay for the other row tile, and `at` is where they begin.
+            auto scores = [&](int32_t t, RingPos at, bool fresh, bool last) {
+                const uint32_t d = tmem + (uint32_t)(t & 1) * 128;
+                const uint32_t qa = q_addr + (two ? (uint32_t)(t & 1) * 16384 : 0u);
+#pragma unroll 1
+                for (int kc = 0; kc < kc_n && ok; ++kc) {
+                    if (fresh) ok = wait0(ms.full + at.idx, at.phase);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const uint32_t ka = ring_addr + (uint32_t)at.idx * kStageBytes;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma(d, sw128_desc(qa + (uint32_t)(kc * x.q_rows) * 128 + kk * 32, 16, 1024),
+                                   sw128_desc(ka + kk * 32, 16, 1024), idesc_s, (kc > 0 || kk > 0) ? 1u : 0u);
+                        if (last) tc_commit(ms.empty + at.idx);
+                    }
+                    __syncwarp();
+                    at.advance(1, S);
+                }
+                if (ok && lane == 0) tc_commit(ms.s_full + (t & 1));
+                __syncwarp();
+                return at;
+            };
+            // O += P(t) V
+            auto values = [&](int32_t t, RingPos at, bool fresh, bool last) {
+                const int32_t tile = two ? t >> 1 : t;
+                const int32_t slot = kAlternate ? t & 1 : 0;
+                const bool first = kAlternate ? t < 2 : t == 0;
+                const uint32_t d = tmem + kOCol + (uint32_t)slot * 128;
+                const uint32_t pa = tmem + (uint32_t)(t & 1) * 128;
+                const int32_t key0 = (w.req.tile0 + w.t0 + tile) * kTile;
+                ok = wait0(ms.p_full + (t & 1), (p_phase >> (t & 1)) & 1u);
+                p_phase ^= 1u << (t & 1);
+                const bool edge = key0 < w.req.lo || key0 + kTile > w.req.L;
+#pragma unroll 1
+                for (int sv = 0; sv < vs_n && ok; ++sv) {
+                    const int32_t h = sv / vc_n, c = sv - h * vc_n;
+                    if (fresh) {
+                        ok = wait0(ms.full + at.idx, at.phase);
+                        if (!ok) break;
+                        if (edge) {
+                            // rows of keys that no node sees
+                            uint8_t* stg = ring + (size_t)at.idx * kStageBytes;
+                            for (int idx = lane; idx < kStageBytes / 16; idx += 32) {
+                                const int32_t key = key0 + h * kVKeys + (idx / 8) % kVKeys;
+                                if (key < w.req.lo || key >= w.req.L)
+                                    *reinterpret_cast<uint4*>(stg + idx * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    if (lane == 0) {
+                        const uint32_t va = ring_addr + (uint32_t)at.idx * kStageBytes;
+#pragma unroll
+                        for (int kk = 0; kk < kVKeys / 16; ++kk)
+                            tc_mma_ta(d + (uint32_t)c * 128, pa + (uint32_t)(h * kVKeys + kk * 16) / 2,
+                                      sw128_desc(va + kk * 2048, 8192, 1024), idesc_o,
+                                      (!first || h > 0 || kk > 0) ? 1u : 0u);
+                        if (last) tc_commit(ms.empty + at.idx);
+                    }
+                    __syncwarp();
+                    at.advance(1, S);
+                }
+                if (ok && lane == 0) tc_commit(ms.o_done + slot);
+                __syncwarp();
+                return at;
+            };
+            if (two) {
+                RingPos v_at{0, 0u}, k_at = pos;
+                pos = scores(0, k_at, true, false);
+                if (ok) scores(1, k_at, false, true);
+#pragma unroll 1
+                for (int32_t j = 0; j < n && ok; ++j) {
+                    v_at = pos;
+                    pos = values(2 * j, v_at, true, false);
+                    k_at = pos;
+                    if (ok && j + 1 < n) pos = scores(2 * j + 2, k_at, true, false);
+                    if (ok) values(2 * j + 1, v_at, false, true);
+                    if (ok && j + 1 < n) scores(2 * j + 3, k_at, false, true);
+                }
+            } else {
+                pos = scores(0, pos, true, true);
+                if (ok && steps > 1) pos = scores(1, pos, true, true);
+#pragma unroll 1
+                for (int32_t t = 0; t < steps && ok; ++t) {
+                    pos = values(t, pos, true, true);
+                    if (ok && t + 2 < steps) pos = scores(t + 2, pos, true, true);
+                }
+            }
+            if (ok && lane == 0) tc_commit(&ms.q_free);
+            __syncwarp();
+        }
+        // our MMAs end before TMEM is freed
+        if (lane == 0) {
+            tc_commit(&ms.drain);
+            const unsigned long long t0 = globaltimer();
+            while (!mbar_test_wait(&ms.drain, 0) && globaltimer() - t0 < p.wait_ns) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ softmax and output
+        const int wg = warp >> 2;
+        const int r128 = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float sl2 = p.scale * kLog2e;
+        const int words = (p.T + 31) / 32;
+        uint32_t s_phase = 0, o_phase = 0;  // bit b: parity of the next phase of buffer / slot b
+        auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+            if (ok) {
+                bool got = true;
+                if (lane == 0) got = ring_wait(bar, parity, abort_flag, p.err, p.wait_ns);
+                ok = __shfl_sync(0xffffffffu, got, 0);
+            }
+            tc_fence_after();
+        };
+        // A failed wait ends the computation, not the walk: the barriers below are met by every thread.
+        for (; !w.done(); w.next(p)) {
+            const int32_t live = live_rows();
+            if (live <= 0) continue;
+            const bool two = kAlternate && live > 128;
+            const int32_t n = w.t1 - w.t0, steps = two ? 2 * n : n;
+            const int32_t ctx = w.req.ctx;
+            const int32_t first_key = (w.req.tile0 + w.t0) * kTile, end_key = (w.req.tile0 + w.t1) * kTile;
+            const int32_t win_end = p.window > 0 ? ctx + w.req.n - p.window : 0;  // keys from here on: no window's edge
+            if (end_key > ctx || first_key < win_end) {
+                named_bar_sync_256();  // the last piece's masks are done with
+                tree_load_parents(p, w.b, w.req.n, ms.par, tid, 256);
+                named_bar_sync_256();
+                tree_walk_nodes(p, w.req, node0, min(p.npt, w.req.n - node0), ms.par, anc_s, lo_s, tid, 256);
+                named_bar_sync_256();
+            }
+            const int32_t row = (two ? wg * 128 : 0) + r128;
+            const bool live_row = row < live;
+            const int32_t nd = row / p.Gc;
+            const uint32_t* anc = anc_s + nd * words;
+            const int32_t slot = kAlternate ? wg : 0;
+            const uint32_t o_addr = tmem + kOCol + (uint32_t)slot * 128 + lanes;
+            const int32_t t_step = kAlternate ? 2 : 1;
+            const int32_t d_here = min(DV, p.D - st.dv * DV);
+            float m2 = -INFINITY, l = 0.f;
+            bool any = false;  // this slot has had a step in the piece
+#pragma unroll 1
+            for (int32_t t = kAlternate ? wg : 0; t < steps && (kAlternate || wg == 0); t += t_step) {
+                const int buf = t & 1;
+                const int32_t key0 = first_key + (two ? t >> 1 : t) * kTile;
+                const bool edge = key0 + kTile > ctx || key0 < win_end;
+                const uint32_t s_addr = tmem + (uint32_t)buf * 128 + lanes;
+                wait_warp(ms.s_full + buf, (s_phase >> buf) & 1u);
+                s_phase ^= 1u << buf;
+                // keys key0 + 32 c .. + 31 that this row sees
+                auto seen = [&](int c) -> uint32_t {
+                    if (!live_row) return 0u;
+                    const int32_t kb = key0 + 32 * c, a = kb - ctx;
+                    uint32_t bits = bit_span(lo_s[nd] - kb, ctx - kb);
+                    if (a <= -32 || a >= w.req.n) return bits;
+                    if (a < 0) return bits | (anc[0] << -a);
+                    const int wd = a >> 5;
+                    return __funnelshift_r(anc[wd], wd + 1 < words ? anc[wd + 1] : 0u, a & 31) | bits;
+                };
+                float mx = -INFINITY;
+                if (ok) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        load32(s_addr + c * 32, r);
+                        if (edge) {
+                            const uint32_t bits = seen(c);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) r[u] = (bits >> u) & 1u ? r[u] : 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) mx = fmaxf(mx, u2f(r[u]));
+                    }
+                }
+                mx *= sl2;
+                const bool grow = live_row && mx > m2 + kRescaleThresh;
+                float alpha = 1.f;
+                if (grow) {
+                    alpha = ex2(m2 - mx);  // 0 from -inf
+                    m2 = mx;
+                    l *= alpha;
+                }
+                bool waited = false;
+                if (any && __any_sync(0xffffffffu, grow)) {
+                    wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
+                    waited = true;
+                    if (ok) {
+#pragma unroll 1
+                        for (int c = 0; c < d_here; c += 32) {
+                            uint32_t r[32];
+                            load32(o_addr + c, r);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) r[u] = f2u(u2f(r[u]) * alpha);
+                            tmem_st32(o_addr + c, r);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float mu = m2 == -INFINITY ? 0.f : m2;
+                if (ok) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        load32(s_addr + c * 32, r);
+                        if (edge) {
+                            const uint32_t bits = seen(c);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) r[u] = (bits >> u) & 1u ? r[u] : 0xFF800000u;
+                        }
+                        uint32_t pk[16];
+                        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) {
+                            const float a = ex2(fmaf(u2f(r[2 * u]), sl2, -mu)), b = ex2(fmaf(u2f(r[2 * u + 1]), sl2, -mu));
+                            sum0 += a;
+                            sum1 += b;
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+                            pk[u] = *reinterpret_cast<const uint32_t*>(&h2);
+                        }
+                        l += sum0 + sum1;
+                        tmem_st16(s_addr + c * 16, pk);  // P over the part of S that is read already
+                    }
+                    tmem_st_wait();
+                }
+                if (any && !waited) wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
+                if (any) o_phase ^= 1u << slot;
+                any = true;
+                tc_fence_before();
+                mbar_arrive(ms.p_full + buf);
+            }
+            if (any) {
+                wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
+                o_phase ^= 1u << slot;
+            }
+            // ---------------------------------------------------------------- output
+            const bool whole = w.whole();
+            const int64_t prow = tree_part_row(p, range, sub, w.slot()) + row;
+            const int32_t node = node0 + nd, head = w.g * p.G + st.gc * p.Gc + (row - nd * p.Gc);
+            const int64_t orow = ((int64_t)w.b * p.T + node) * p.Hq + head;
+            float f0, f1 = 0.f, lse2;
+            if (two) {
+                f0 = l > 0.f ? 1.f / l : 0.f;
+                lse2 = l > 0.f ? m2 + __log2f(l) : -INFINITY;
+            } else {
+                tc_fence_before();
+                ms.m[wg][r128] = m2;
+                ms.l[wg][r128] = l;
+                named_bar_sync_256();
+                tc_fence_after();
+                const float ma = ms.m[0][r128], mb = ms.m[1][r128];
+                const float mm = fmaxf(ma, mb);
+                const float wa = ma == -INFINITY ? 0.f : ex2(ma - mm), wb = mb == -INFINITY ? 0.f : ex2(mb - mm);
+                const float tot = ms.l[0][r128] * wa + ms.l[1][r128] * wb;
+                const float inv = tot > 0.f ? 1.f / tot : 0.f;
+                f0 = wa * inv;
+                f1 = wb * inv;
+                lse2 = tot > 0.f ? mm + __log2f(tot) : -INFINITY;
+            }
+            if (live_row && st.dv == 0 && (two || wg == 0)) {
+                const float lse = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
+                if (!whole)
+                    p.part_lse[prow] = lse;
+                else if (p.lse)
+                    p.lse[orow] = lse;
+            }
+            if (live_row && st.dv != 0 && wg == 0 && !whole) p.part_lse[prow] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
+            // two row tiles: a warpgroup writes its own rows; one: each half of the columns
+            const int32_t c_begin = two ? 0 : wg * (DV / 2), c_end = min(d_here, two ? DV : c_begin + DV / 2);
+            const uint32_t own = tmem + kOCol + (two ? (uint32_t)slot * 128 : 0u) + lanes;
+            const bool second = kAlternate && !two && steps > 1;
+            if (ok) {
+#pragma unroll 1
+                for (int32_t c = c_begin; c < c_end; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(own + c, r);
+                    tmem_ld_wait();
+                    reg_fence16(r);
+                    float o[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) o[u] = u2f(r[u]) * f0;
+                    if (second) {
+                        tmem_ld16(own + 128 + c, r);
+                        tmem_ld_wait();
+                        reg_fence16(r);
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) o[u] = fmaf(u2f(r[u]), f1, o[u]);
+                    }
+                    if (!live_row) continue;
+                    if (!whole) {
+                        float4* dst = reinterpret_cast<float4*>(p.part_out + prow * DV + c);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                    } else {
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * u], o[2 * u + 1]);
+                            pk[u] = *reinterpret_cast<const uint32_t*>(&h2);
+                        }
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * p.D +
+                                                              st.dv * DV + c);
+                        dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (!two) named_bar_sync_256();  // O and the sums are read before the next piece's steps
+        }
+    }
+    // ---------------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+bool encode(EncodeTiledFn enc, CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box)
+{
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DV>
+cudaError_t launch_dv(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeAttnParams& p,
+                      cudaStream_t stream)
+{
+    TcShape x;
+    x.q_rows = (p.rows + 7) / 8 * 8;
+    x.box = 8;
+    while (x.box < 64 && p.page_size % (2 * x.box) == 0) x.box *= 2;
+    const int32_t q_bytes = (p.D + 63) / 64 * x.q_rows * 128;
+    const int32_t misc = (int32_t)sizeof(TcMisc) + p.npt * 4 * (1 + (p.T + 31) / 32);
+    x.stages = std::min(kMaxStages, (kSmemMax - 1024 - q_bytes - misc) / kStageBytes);
+    // Q's 128- or 256-row reads past its last row end inside the ring
+    if (x.stages < 4) return cudaErrorInvalidConfiguration;
+    const int32_t bytes = 1024 + q_bytes + x.stages * kStageBytes + misc;
+    cudaError_t e = cudaFuncSetAttribute(tree_attn_tc_kernel<DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    tree_attn_tc_kernel<DV><<<p.ranges * p.n_sub, kThreads, bytes, stream>>>(tq, tk, tv, p, x);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tree_tc_supports(const dflash_dims* d)
+{
+    const int64_t most = int64_t(1) << 39;  // elements: a tensor map's strides end at 2^40 bytes
+    if (d->dtype != DFLASH_BF16) return false;
+    if (d->kv_stride_slot <= 0 || (d->num_kv_heads > 1 && d->kv_stride_head <= 0) ||
+        (d->num_pages > 1 && d->kv_stride_page <= 0))
+        return false;
+    return d->kv_stride_slot < most && d->kv_stride_head < most && d->kv_stride_page < most;
+}
+
+cudaError_t launch_tree_attn_tc(const TreeAttnParams& p, cudaStream_t stream)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    int32_t box = 8;
+    while (box < 64 && p.page_size % (2 * box) == 0) box *= 2;
+    CUtensorMap tq, tk, tv;
+    const cuuint64_t qd[3] = {(cuuint64_t)p.D, (cuuint64_t)p.Hq, (cuuint64_t)p.B * p.T};
+    const cuuint64_t qs[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.Hq * p.D * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)p.Gc, (cuuint32_t)p.npt};
+    // a stride that is never taken (one head, one page) may be anything: the tensor map wants a plain one
+    const int64_t sh = p.Hkv > 1 ? p.sh : p.D, sp = p.num_pages > 1 ? p.sp : p.ss * p.page_size;
+    const cuuint64_t kd[4] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv, (cuuint64_t)p.page_size, (cuuint64_t)p.num_pages};
+    const cuuint64_t ks[3] = {(cuuint64_t)sh * 2, (cuuint64_t)p.ss * 2, (cuuint64_t)sp * 2};
+    const cuuint32_t kb[4] = {64, 1, (cuuint32_t)box, 1};
+    if (!encode(enc, &tq, p.q, 3, qd, qs, qb) || !encode(enc, &tk, p.k, 4, kd, ks, kb) ||
+        !encode(enc, &tv, p.v, 4, kd, ks, kb))
+        return cudaErrorInvalidValue;
+    switch (p.DV) {
+    case 64: return launch_dv<64>(tq, tk, tv, p, stream);
+    case 128: return launch_dv<128>(tq, tk, tv, p, stream);
+    default: return launch_dv<256>(tq, tk, tv, p, stream);
+    }
+}
+
 }  // namespace dflash

@@ -23,7 +23,7 @@ pytestmark = pytest.mark.gpu
 
 U16, U32 = 2.0 ** -8, 2.0 ** -24
 GUARD = 1024
-KERNELS16 = ("simt",)
+KERNELS16 = ("simt", "tc")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -147,7 +147,7 @@ class Tree:
         return dfl.read_error(self.ws)
 
 
-BOTH = [("simt", torch.float32), ("simt", torch.bfloat16)]
+BOTH = [("simt", torch.float32), ("simt", torch.bfloat16), ("tc", torch.bfloat16)]
 
 
 

@@ -93,25 +93,43 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr));
 }
 
-// Loads 32 columns and waits; later uses of the registers are ordered after the wait.
-__device__ __forceinline__ void load32(uint32_t taddr, uint32_t (&r)[32])
+// Orders later uses of loaded registers after the wait for the loads.
+__device__ __forceinline__ void reg_fence32(uint32_t (&r)[32])
 {
-    tmem_ld32(taddr, r);
-    tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 32 bytes, a whole sector, in one store.
+__device__ __forceinline__ void store_f8(float* dst, const float* v)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]),
+                 "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
 
 // D (TMEM) (+)= A (TMEM, bf16 pairs) . B (shared memory)
@@ -522,20 +540,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int wd = a >> 5;
                     return __funnelshift_r(anc[wd], wd + 1 < words ? anc[wd + 1] : 0u, a & 31) | bits;
                 };
+                // rows of scores in registers, 64 columns at a time: enough independent values to fill the pipes (with
+                // all 128 held across the rescale the compiler spilled)
+                auto load64 = [&](int h, uint32_t (&r)[2][32]) {
+                    tmem_ld32(s_addr + h * 64, r[0]);
+                    tmem_ld32(s_addr + h * 64 + 32, r[1]);
+                    tmem_ld_wait();
+                    reg_fence32(r[0]);
+                    reg_fence32(r[1]);
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t bits = seen(2 * h + c);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) r[c][u] = (bits >> u) & 1u ? r[c][u] : 0xFF800000u;
+                        }
+                    }
+                };
                 float mx = -INFINITY;
                 if (ok) {
+                    float mc[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mc[i] = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        load32(s_addr + c * 32, r);
-                        if (edge) {
-                            const uint32_t bits = seen(c);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[2][32];
+                        load64(h, r);
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) r[u] = (bits >> u) & 1u ? r[u] : 0xFF800000u;
-                        }
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) mx = fmaxf(mx, u2f(r[u]));
+                            for (int u = 0; u < 32; u += 16)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    mc[i] = fmaxf(fmaxf(mc[i], u2f(r[c][u + i])), u2f(r[c][u + 8 + i]));
                     }
+                    mx = fmaxf(fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])),
+                               fmaxf(fmaxf(mc[4], mc[5]), fmaxf(mc[6], mc[7])));
                 }
                 mx *= sl2;
                 const bool grow = live_row && mx > m2 + kRescaleThresh;
@@ -552,39 +592,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ok) {
 #pragma unroll 1
                         for (int c = 0; c < d_here; c += 32) {
-                            uint32_t r[32];
-                            load32(o_addr + c, r);
+                            uint32_t o[16];
+                            tmem_ld16(o_addr + c, o);
+                            tmem_ld_wait();
+                            reg_fence16(o);
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) r[u] = f2u(u2f(r[u]) * alpha);
-                            tmem_st32(o_addr + c, r);
+                            for (int u = 0; u < 16; ++u) o[u] = f2u(u2f(o[u]) * alpha);
+                            tmem_st16(o_addr + c, o);
                         }
                         tmem_st_wait();
                     }
                 }
                 const float mu = m2 == -INFINITY ? 0.f : m2;
                 if (ok) {
+                    const uint64_t scale2 = pack2(sl2, sl2), shift2 = pack2(-mu, -mu);
+                    uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        load32(s_addr + c * 32, r);
-                        if (edge) {
-                            const uint32_t bits = seen(c);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[2][32];
+                        load64(h, r);
+                        uint32_t pk[2][16];
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) r[u] = (bits >> u) & 1u ? r[u] : 0xFF800000u;
-                        }
-                        uint32_t pk[16];
-                        float sum0 = 0.f, sum1 = 0.f;
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) {
-                            const float a = ex2(fmaf(u2f(r[2 * u]), sl2, -mu)), b = ex2(fmaf(u2f(r[2 * u + 1]), sl2, -mu));
-                            sum0 += a;
-                            sum1 += b;
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
-                            pk[u] = *reinterpret_cast<const uint32_t*>(&h2);
-                        }
-                        l += sum0 + sum1;
-                        tmem_st16(s_addr + c * 16, pk);  // P over the part of S that is read already
+                            for (int u = 0; u < 16; ++u) {
+                                float a, b;
+                                unpack2(fma2(pack2(u2f(r[c][2 * u]), u2f(r[c][2 * u + 1])), scale2, shift2), a, b);
+                                a = ex2(a);
+                                b = ex2(b);
+                                sum[u & 3] = add2(sum[u & 3], pack2(a, b));
+                                const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+                                pk[c][u] = *reinterpret_cast<const uint32_t*>(&h2);
+                            }
+                        // P over S: columns 32 h .. of the half that is read, and of the first half
+                        tmem_st16(s_addr + h * 32, pk[0]);
+                        tmem_st16(s_addr + h * 32 + 16, pk[1]);
                     }
+                    float a, b;
+                    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+                    l += a + b;
                     tmem_st_wait();
                 }
                 if (any && !waited) wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
@@ -652,9 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!live_row) continue;
                     if (!whole) {
-                        float4* dst = reinterpret_cast<float4*>(p.part_out + prow * DV + c);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                        float* dst = p.part_out + prow * DV + c;
+                        store_f8(dst, o);
+                        store_f8(dst + 8, o + 8);
                     } else {
                         uint32_t pk[8];
 #pragma unroll

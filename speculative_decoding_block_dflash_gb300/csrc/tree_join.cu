@@ -4,9 +4,9 @@
 // Pairs that one range holds whole are final already. A request with a bad length or tree size gets its
 // zeros here.
 //
-// A CTA takes kRows rows of one (pair, query tile); a thread owns a float4 of a row, reads the row's chunk lse
-// values itself and keeps eight partial loads in flight. Launched as a programmatic
-// dependent of the attention kernel.
+// A warp takes a row: its lanes read the partials' lse values (32 at a time) and form the weights, then stream the
+// partial rows, eight loads in flight. Launched as a programmatic dependent of the attention kernel; the deal of
+// tiles to ranges is worked out before the wait for it. Bound: the partials' bytes out of L2.
 #include <cmath>
 
 #include "tree_attn.cuh"
@@ -15,89 +15,110 @@ namespace dflash {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
-__global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParams p, int32_t rows_per_cta)
+template <int V>  // floats per lane: DV <= 32 V
+__global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParams p)
 {
-    __shared__ int64_t sh_first, sh_total;
-    cudaGridDependencySynchronize();
+    __shared__ int32_t sh_r0, sh_parts;
     const int32_t pair = blockIdx.x;
     const int32_t b = pair / p.Hkv, g = pair % p.Hkv;
     const int32_t sub = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const SubTile st = sub_tile(p, sub);
     const TreeReq rq = tree_request(p, b);
     const int32_t node0 = st.rt * p.npt;
     if (rq.bad && g == 0 && sub == 0 && blockIdx.z == 0 && threadIdx.x == 0) raise_error(p.err, tree_request_error(p, rq));
-    if (rq.nt == 0 && !rq.bad) return;
-    if (!rq.bad && node0 >= rq.n) return;
-    const int lanes = p.DV / 4;
-    const int d_here = min(p.DV, p.D - st.dv * p.DV);
+    const int32_t n_here = rq.bad ? p.T : rq.n;
+    const int32_t live = min(p.npt, n_here - node0) * p.Gc;
     int32_t r0 = 0, parts = 0;
-    if (!rq.bad) {
-        if (threadIdx.x < 32) {
-            const int64_t before = tree_tiles_before(p, b), all = tree_tiles_before(p, p.B);
-            if (threadIdx.x == 0) {
-                sh_first = before + (int64_t)g * rq.nt;
-                sh_total = all;
+    if (rq.nt > 0 && live > 0) {
+        if (warp == 0) {
+            const int64_t first = tree_tiles_before(p, b) + (int64_t)g * rq.nt, total = tree_tiles_before(p, p.B);
+            const int32_t used = ranges_used(p, total);
+            if (lane == 0) {
+                sh_r0 = range_of(total, used, first);
+                sh_parts = range_of(total, used, first + rq.nt - 1) - sh_r0 + 1;
             }
         }
         __syncthreads();
-        const int64_t total = sh_total;
-        const int32_t used = ranges_used(p, total);
-        r0 = range_of(total, used, sh_first);
-        parts = range_of(total, used, sh_first + rq.nt - 1) - r0 + 1;
-        if (parts == 1) return;
+        r0 = sh_r0;
+        parts = sh_parts;
     }
-    const int32_t n_here = rq.bad ? p.T : rq.n;
-    const int32_t live = min(p.npt, n_here - node0) * p.Gc;
-    const int32_t row_end = min(live, (int32_t)(blockIdx.z + 1) * rows_per_cta);
-    for (int32_t item = blockIdx.z * rows_per_cta * lanes + threadIdx.x; item < row_end * lanes; item += kThreads) {
-        const int32_t row = item / lanes, d0 = (item - row * lanes) * 4;
+    cudaGridDependencySynchronize();
+    if (live <= 0 || parts == 1 || (parts == 0 && !rq.bad)) return;
+    const int32_t d_here = min(p.DV, p.D - st.dv * p.DV);
+    const int32_t d0 = lane * V;
+    const bool has = d0 < d_here;
+    for (int32_t row = blockIdx.z * kWarps + warp; row < live; row += gridDim.z * kWarps) {
         float m = -INFINITY;
-        for (int c = 0; c < parts; ++c)
+        for (int32_t c = lane; c < parts; c += 32)
             m = fmaxf(m, __ldg(p.part_lse + tree_part_row(p, r0 + c, sub, c == 0 ? 1 : 0) + row));
-        float t = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (m != -INFINITY && d0 < d_here) {
-            for (int c0 = 0; c0 < parts; c0 += 8) {
-                float w[8];
-                float4 v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int c = c0 + k;
-                    const int64_t at = tree_part_row(p, r0 + min(c, parts - 1), sub, c == 0 ? 1 : 0) + row;
-                    const float l = c < parts ? __ldg(p.part_lse + at) : -INFINITY;
-                    w[k] = l == -INFINITY ? 0.f : expf(l - m);
-                    v[k] = w[k] > 0.f ? __ldg(reinterpret_cast<const float4*>(p.part_out + at * p.DV + d0))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        float t = 0.f, acc[V];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    t += w[k];
-                    acc.x = fmaf(w[k], v[k].x, acc.x);
-                    acc.y = fmaf(w[k], v[k].y, acc.y);
-                    acc.z = fmaf(w[k], v[k].z, acc.z);
-                    acc.w = fmaf(w[k], v[k].w, acc.w);
+        for (int u = 0; u < V; ++u) acc[u] = 0.f;
+        if (m != -INFINITY) {
+            for (int32_t c0 = 0; c0 < parts; c0 += 32) {
+                const int32_t mine = c0 + lane;
+                const float lse = mine < parts
+                                      ? __ldg(p.part_lse + tree_part_row(p, r0 + mine, sub, mine == 0 ? 1 : 0) + row)
+                                      : -INFINITY;
+                const float w = lse == -INFINITY ? 0.f : expf(lse - m);
+                const int32_t here = min(32, parts - c0);
+                for (int32_t c1 = 0; c1 < here; c1 += 8) {
+                    float x[8][V];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int32_t c = c0 + c1 + k;
+                        const bool on = c1 + k < here && has;
+                        const float* src = p.part_out + (tree_part_row(p, r0 + min(c, parts - 1), sub, c == 0 ? 1 : 0) + row) * p.DV + d0;
+#pragma unroll
+                        for (int u = 0; u < V; u += V < 4 ? 2 : 4) {
+                            if (V < 4) {
+                                const float2 y = on ? __ldg(reinterpret_cast<const float2*>(src + u)) : make_float2(0.f, 0.f);
+                                x[k][u] = y.x;
+                                x[k][u + 1] = y.y;
+                            } else {
+                                const float4 y = on ? __ldg(reinterpret_cast<const float4*>(src + u))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                                x[k][u] = y.x;
+                                x[k][u + 1] = y.y;
+                                x[k][(u + 2) % V] = y.z;
+                                x[k][(u + 3) % V] = y.w;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        // (a partial without a visible key is 0 and so is its weight)
+                        const float wk = __shfl_sync(0xffffffffu, w, (c1 + k) & 31);
+                        const float wz = c1 + k < here ? wk : 0.f;
+                        t += wz;
+#pragma unroll
+                        for (int u = 0; u < V; ++u) acc[u] = fmaf(wz, x[k][u], acc[u]);
+                    }
                 }
             }
         }
-        if (d0 >= d_here) continue;
         const bool empty = !(t > 0.f);
         const float inv = empty ? 0.f : 1.f / t;
         const int32_t node = node0 + row / p.Gc, head = g * p.G + st.gc * p.Gc + row % p.Gc;
         const int64_t orow = ((int64_t)b * p.T + node) * p.Hq + head;
         const int64_t o = orow * p.D + st.dv * p.DV + d0;
-        if (p.dtype == DFLASH_BF16) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            uint2 pk;
-            pk.x = *reinterpret_cast<const uint32_t*>(&lo);
-            pk.y = *reinterpret_cast<const uint32_t*>(&hi);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o) = pk;
-        } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (has) {
+#pragma unroll
+            for (int u = 0; u < V; u += 2) {
+                if (p.dtype == DFLASH_BF16)
+                    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + o + u) =
+                        __floats2bfloat162_rn(acc[u] * inv, acc[u + 1] * inv);
+                else
+                    *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o + u) =
+                        make_float2(acc[u] * inv, acc[u + 1] * inv);
+            }
         }
-        if (d0 == 0 && st.dv == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : m + logf(t);
+        if (lane == 0 && st.dv == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : m + logf(t);
     }
 }
 
@@ -105,9 +126,8 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
 
 cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream)
 {
-    const int32_t rows_per_cta = 8;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv), (unsigned)p.n_sub, (unsigned)((p.rows + rows_per_cta - 1) / rows_per_cta));
+    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv), (unsigned)p.n_sub, (unsigned)((p.rows + kWarps - 1) / kWarps));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -115,7 +135,11 @@ cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel, p, rows_per_cta);
+    // a lane's floats: the narrowest that cover the partial's row (DV is a multiple of 16)
+    if (p.DV <= 64) return cudaLaunchKernelEx(&cfg, tree_join_kernel<2>, p);
+    if (p.DV <= 128) return cudaLaunchKernelEx(&cfg, tree_join_kernel<4>, p);
+    if (p.DV <= 256) return cudaLaunchKernelEx(&cfg, tree_join_kernel<8>, p);
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<16>, p);
 }
 
 }  // namespace dflash

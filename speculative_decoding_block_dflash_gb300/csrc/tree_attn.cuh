@@ -40,31 +40,38 @@ __device__ __forceinline__ uint32_t tree_request_error(const TreeAttnParams& p, 
     return (r.n < 0 || r.n > p.T) ? DFLASH_DEVERR_TREE : DFLASH_DEVERR_SEQ_LEN;
 }
 
-// Key tiles of all (request, KV head) pairs before request b (b = B: of all). Called by a whole warp.
-__device__ __forceinline__ int64_t tree_tiles_before(const TreeAttnParams& p, int32_t b_end)
+// The deal counts in units of a key tile's time. A pair of nt tiles weighs kPairCost + nt: its first units stand for
+// loading its queries, filling the pipeline and writing its result, so that ranges of many short pairs get fewer
+// tiles.
+constexpr int32_t kPairCost = 4;
+
+__device__ __forceinline__ int64_t tree_weight(const TreeReq& r) { return r.nt > 0 ? r.nt + kPairCost : 0; }
+
+// Weight of all (request, KV head) pairs before request b (b = B: of all). Called by a whole warp.
+__device__ __forceinline__ int64_t tree_weight_before(const TreeAttnParams& p, int32_t b_end)
 {
     const int lane = threadIdx.x & 31;
     int64_t sum = 0;
 #pragma unroll 1
-    for (int32_t b = lane; b < b_end; b += 32) sum += tree_request(p, b).nt;
+    for (int32_t b = lane; b < b_end; b += 32) sum += tree_weight(tree_request(p, b));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     return sum * p.Hkv;
 }
 
-// Ranges in use: none is empty, so that a pair's partials lie in consecutive ranges.
+// Ranges in use: none has weight 0, so that a pair's partials lie in consecutive ranges.
 __device__ __forceinline__ int32_t ranges_used(const TreeAttnParams& p, int64_t total)
 {
     return (int32_t)(total < p.ranges ? total : p.ranges);
 }
 
-// First tile of range r when `total` tiles are dealt to `ranges` ranges.
+// Where range r begins when a weight of `total` is dealt to `ranges` ranges.
 __device__ __forceinline__ int64_t range_begin(int64_t total, int32_t ranges, int32_t r)
 {
     return total * r / ranges;
 }
 
-// The range that holds tile x.
+// The range that holds unit x of the weight.
 __device__ __forceinline__ int32_t range_of(int64_t total, int32_t ranges, int64_t x)
 {
     int32_t r = (int32_t)(x * ranges / total);
@@ -75,22 +82,25 @@ __device__ __forceinline__ int32_t range_of(int64_t total, int32_t ranges, int64
 
 // A walk over the pieces of one range: a piece is the part of one (request, KV head) pair's tiles that lies in it.
 struct PieceWalk {
-    int64_t left;     // tiles of the range still to come, this piece's among them
-    int32_t b, g, t0;  // the piece: pair (b, g), tiles [t0, t1) of the pair's
-    int32_t t1;
+    int64_t left;      // weight of the range still to come, this piece's part included
+    int32_t b, g, at;  // the pair (b, g), and where in its weight the piece begins
+    int32_t t0, t1;    // the piece: tiles [t0, t1) of the pair's
     TreeReq req;
 
-    __device__ __forceinline__ void set_end()
+    __device__ __forceinline__ void cut()
     {
-        const int64_t rest = req.nt - t0;
-        t1 = t0 + (int32_t)(left < rest ? left : rest);
+        const int64_t weight = tree_weight(req);
+        const int64_t end = left < weight - at ? at + left : weight;
+        t0 = max(0, at - kPairCost);
+        t1 = max(0, (int32_t)end - kPairCost);
+        left -= end - at;
     }
-    __device__ __forceinline__ bool done() const { return left <= 0; }
+    __device__ __forceinline__ bool done() const { return t1 <= t0; }
     // Start of range r (a whole warp calls it).
     __device__ __forceinline__ void start(const TreeAttnParams& p, int32_t r)
     {
         const int lane = threadIdx.x & 31;
-        const int64_t total = tree_tiles_before(p, p.B);
+        const int64_t total = tree_weight_before(p, p.B);
         const int32_t used = ranges_used(p, total);
         int64_t x = 0;
         left = 0;
@@ -98,13 +108,13 @@ struct PieceWalk {
             x = range_begin(total, used, r);
             left = range_begin(total, used, r + 1) - x;
         }
-        b = g = t0 = t1 = 0;
+        b = g = at = t0 = t1 = 0;
         req.n = req.ctx = req.L = req.lo = req.tile0 = req.nt = 0;
         req.bad = false;
         if (left <= 0) return;
 #pragma unroll 1
         for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
-            const int64_t mine = b0 + lane < p.B ? (int64_t)tree_request(p, b0 + lane).nt * p.Hkv : 0;
+            const int64_t mine = b0 + lane < p.B ? tree_weight(tree_request(p, b0 + lane)) * p.Hkv : 0;
             int64_t incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -121,26 +131,29 @@ struct PieceWalk {
             x -= __shfl_sync(0xffffffffu, incl, 31);
         }
         req = tree_request(p, b);
-        g = (int32_t)(x / req.nt);
-        t0 = (int32_t)(x - (int64_t)g * req.nt);
-        set_end();
+        g = (int32_t)(x / tree_weight(req));
+        at = (int32_t)(x - (int64_t)g * tree_weight(req));
+        cut();
+        if (done()) next(p);  // the range begins in a pair's first units and ends there, or it does not reach a tile
     }
+    // The next piece that holds a tile, if any (done() otherwise).
     __device__ __forceinline__ void next(const TreeAttnParams& p)
     {
-        left -= t1 - t0;
-        if (left <= 0) return;
-        t0 = 0;
-        if (++g == p.Hkv) {
-            g = 0;
-            do {
-                ++b;
-                req = tree_request(p, b);
-            } while (req.nt == 0);
+        t0 = t1 = 0;
+        while (left > 0 && t1 <= t0) {
+            at = 0;
+            if (++g == p.Hkv) {
+                g = 0;
+                do {
+                    ++b;
+                    req = tree_request(p, b);
+                } while (req.nt == 0);
+            }
+            cut();
         }
-        set_end();
     }
     // Whether the piece is a whole pair (its result is final), and its partial's slot otherwise: the pair's
-    // first piece ends a range and takes slot 1, a later one begins a range and takes slot 0.
+    // first piece takes slot 1, a later one slot 0 (a range holds at most one of each that is not whole).
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == req.nt; }
     __device__ __forceinline__ int slot() const { return t0 == 0 ? 1 : 0; }
 };

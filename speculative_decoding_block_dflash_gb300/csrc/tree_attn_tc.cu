@@ -72,7 +72,7 @@ struct TcShape {
 struct TcMisc {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_free;
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
     uint64_t drain;
     uint32_t tmem;
     int32_t abort;
@@ -141,6 +141,18 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
         : "memory");
+}
+
+// One thread of the warp, always the same.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
 }
 
 // A ring position that advances by `by` stages.
@@ -226,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ms.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(ms.s_full + i, 1);
+            mbar_init(ms.p_half + i, 128);
             mbar_init(ms.p_full + i, 128);
             mbar_init(ms.o_done + i, 1);
         }
@@ -360,15 +373,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------------ MMA issuer
         constexpr uint32_t idesc_s = make_idesc(128, kTile, 0, 0);
         constexpr uint32_t idesc_o = make_idesc(128, kVN, 0, 1);
-        const uint32_t q_addr = smem_u32(q_s), ring_addr = smem_u32(ring);
+        // Descriptors are made once: a later operand is its base plus an offset in 16-byte units. Everything about an
+        // MMA but the issue itself is the same for the whole warp, so that it lies in uniform registers, where the
+        // instruction wants it; with the operands worked out by one thread an MMA took about 150 cycles to issue.
+        const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024), k_desc = sw128_desc(smem_u32(ring), 16, 1024),
+                       v_desc = sw128_desc(smem_u32(ring), 8192, 1024);
+        const uint32_t q_chunk = (uint32_t)x.q_rows * 8;  // one 64-dim chunk of Q
         RingPos pos{0, 0u};
         uint32_t q_phase = 0, p_phase = 0;  // p_phase: bit b = parity of the next P in buffer b
         auto wait0 = [&](uint64_t* bar, uint32_t parity) -> bool {
-            bool got = true;
-            if (lane == 0) got = ring_wait(bar, parity, abort_flag, p.err, p.wait_ns);
-            got = __shfl_sync(0xffffffffu, got, 0);
-            tc_fence_after();
-            return got;
+            return __all_sync(0xffffffffu, ring_wait(bar, parity, abort_flag, p.err, p.wait_ns));
         };
         for (; !w.done() && ok; w.next(p)) {
             const int32_t live = live_rows();
@@ -382,23 +396,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             // last (they are released). Otherwise the stages stay for the other row tile, and `at` is where they begin.
             auto scores = [&](int32_t t, RingPos at, bool fresh, bool last) {
                 const uint32_t d = tmem + (uint32_t)(t & 1) * 128;
-                const uint32_t qa = q_addr + (two ? (uint32_t)(t & 1) * 16384 : 0u);
+                uint64_t qd = q_desc + (two ? (uint32_t)(t & 1) * 1024 : 0u);
 #pragma unroll 1
                 for (int kc = 0; kc < kc_n && ok; ++kc) {
                     if (fresh) ok = wait0(ms.full + at.idx, at.phase);
                     if (!ok) break;
-                    if (lane == 0) {
-                        const uint32_t ka = ring_addr + (uint32_t)at.idx * kStageBytes;
+                    const uint64_t kd = k_desc + (uint32_t)at.idx * (kStageBytes / 16);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            tc_mma(d, sw128_desc(qa + (uint32_t)(kc * x.q_rows) * 128 + kk * 32, 16, 1024),
-                                   sw128_desc(ka + kk * 32, 16, 1024), idesc_s, (kc > 0 || kk > 0) ? 1u : 0u);
+                            tc_mma(d, qd + 2 * kk, kd + 2 * kk, idesc_s, (kc > 0 || kk > 0) ? 1u : 0u);
                         if (last) tc_commit(ms.empty + at.idx);
                     }
                     __syncwarp();
+                    qd += q_chunk;
                     at.advance(1, S);
                 }
-                if (ok && lane == 0) tc_commit(ms.s_full + (t & 1));
+                if (ok && elect_one()) tc_commit(ms.s_full + (t & 1));
                 __syncwarp();
                 return at;
             };
@@ -410,12 +424,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t d = tmem + kOCol + (uint32_t)slot * 128;
                 const uint32_t pa = tmem + (uint32_t)(t & 1) * 128;
                 const int32_t key0 = (w.req.tile0 + w.t0 + tile) * kTile;
-                ok = wait0(ms.p_full + (t & 1), (p_phase >> (t & 1)) & 1u);
-                p_phase ^= 1u << (t & 1);
+                // the first 64 keys' probabilities come ahead of the rest
+                ok = wait0(ms.p_half + (t & 1), (p_phase >> (t & 1)) & 1u);
+                tc_fence_after();
+                if (DV == 64 && ok) {  // a V stage is 128 keys
+                    ok = wait0(ms.p_full + (t & 1), (p_phase >> (t & 1)) & 1u);
+                    tc_fence_after();
+                }
                 const bool edge = key0 < w.req.lo || key0 + kTile > w.req.L;
 #pragma unroll 1
                 for (int sv = 0; sv < vs_n && ok; ++sv) {
                     const int32_t h = sv / vc_n, c = sv - h * vc_n;
+                    if (DV != 64 && sv == vc_n) {
+                        ok = wait0(ms.p_full + (t & 1), (p_phase >> (t & 1)) & 1u);
+                        tc_fence_after();
+                        if (!ok) break;
+                    }
                     if (fresh) {
                         ok = wait0(ms.full + at.idx, at.phase);
                         if (!ok) break;
@@ -431,19 +455,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                         }
                     }
-                    if (lane == 0) {
-                        const uint32_t va = ring_addr + (uint32_t)at.idx * kStageBytes;
+                    const uint64_t vd = v_desc + (uint32_t)at.idx * (kStageBytes / 16);
+                    const uint32_t dc = d + (uint32_t)c * 128, ph = pa + (uint32_t)(h * kVKeys) / 2;
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kVKeys / 16; ++kk)
-                            tc_mma_ta(d + (uint32_t)c * 128, pa + (uint32_t)(h * kVKeys + kk * 16) / 2,
-                                      sw128_desc(va + kk * 2048, 8192, 1024), idesc_o,
-                                      (!first || h > 0 || kk > 0) ? 1u : 0u);
+                            tc_mma_ta(dc, ph + kk * 8, vd + kk * 128, idesc_o, (!first || h > 0 || kk > 0) ? 1u : 0u);
                         if (last) tc_commit(ms.empty + at.idx);
                     }
                     __syncwarp();
                     at.advance(1, S);
                 }
-                if (ok && lane == 0) tc_commit(ms.o_done + slot);
+                p_phase ^= 1u << (t & 1);
+                if (ok && elect_one()) tc_commit(ms.o_done + slot);
                 __syncwarp();
                 return at;
             };
@@ -469,11 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ok && t + 2 < steps) pos = scores(t + 2, pos, true, true);
                 }
             }
-            if (ok && lane == 0) tc_commit(&ms.q_free);
+            if (ok && elect_one()) tc_commit(&ms.q_free);
             __syncwarp();
         }
         // our MMAs end before TMEM is freed
-        if (lane == 0) {
+        if (elect_one()) {
             tc_commit(&ms.drain);
             const unsigned long long t0 = globaltimer();
             while (!mbar_test_wait(&ms.drain, 0) && globaltimer() - t0 < p.wait_ns) {
@@ -604,11 +628,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float mu = m2 == -INFINITY ? 0.f : m2;
-                if (ok) {
-                    const uint64_t scale2 = pack2(sl2, sl2), shift2 = pack2(-mu, -mu);
-                    uint64_t sum[4] = {0, 0, 0, 0};
+                const uint64_t scale2 = pack2(sl2, sl2), shift2 = pack2(-mu, -mu);
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2; ++h) {
+                    if (ok) {
                         uint32_t r[2][32];
                         load64(h, r);
                         uint32_t pk[2][16];
@@ -627,17 +651,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // P over S: columns 32 h .. of the half that is read, and of the first half
                         tmem_st16(s_addr + h * 32, pk[0]);
                         tmem_st16(s_addr + h * 32 + 16, pk[1]);
+                        tmem_st_wait();
                     }
-                    float a, b;
-                    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
-                    l += a + b;
-                    tmem_st_wait();
+                    // every phase of o_done is waited for once, so that its parity tells them apart
+                    if (h == 0 && any && !waited) wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
+                    tc_fence_before();
+                    mbar_arrive((h == 0 ? ms.p_half : ms.p_full) + buf);
                 }
-                if (any && !waited) wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
                 if (any) o_phase ^= 1u << slot;
                 any = true;
-                tc_fence_before();
-                mbar_arrive(ms.p_full + buf);
+                float a, b;
+                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+                l += a + b;
             }
             if (any) {
                 wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);

@@ -7,6 +7,7 @@
 // A warp takes a row: its lanes read the partials' lse values (32 at a time) and form the weights, then stream the
 // partial rows, eight loads in flight. Launched as a programmatic dependent of the attention kernel; the deal of
 // tiles to ranges is worked out before the wait for it. Bound: the partials' bytes out of L2.
+#include <algorithm>
 #include <cmath>
 
 #include "tree_attn.cuh"
@@ -34,11 +35,11 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
     int32_t r0 = 0, parts = 0;
     if (rq.nt > 0 && live > 0) {
         if (warp == 0) {
-            const int64_t first = tree_tiles_before(p, b) + (int64_t)g * rq.nt, total = tree_tiles_before(p, p.B);
+            const int64_t first = tree_weight_before(p, b) + g * tree_weight(rq), total = tree_weight_before(p, p.B);
             const int32_t used = ranges_used(p, total);
             if (lane == 0) {
-                sh_r0 = range_of(total, used, first);
-                sh_parts = range_of(total, used, first + rq.nt - 1) - sh_r0 + 1;
+                sh_r0 = range_of(total, used, first + kPairCost);  // its tiles follow its fixed cost
+                sh_parts = range_of(total, used, first + tree_weight(rq) - 1) - sh_r0 + 1;
             }
         }
         __syncthreads();
@@ -127,7 +128,11 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
 cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv), (unsigned)p.n_sub, (unsigned)((p.rows + kWarps - 1) / kWarps));
+    // about one wave of warps: a warp then takes several rows of a large call, one of a small one
+    const int64_t wave = (int64_t)device_sm_count() * 4, tiles = (int64_t)p.B * p.Hkv * p.n_sub;
+    const int64_t most = (p.rows + kWarps - 1) / kWarps;
+    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv), (unsigned)p.n_sub,
+                       (unsigned)std::max<int64_t>(1, std::min(most, (wave + tiles - 1) / tiles)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -580,6 +580,9 @@ def selector_walk(pred_codebook: torch.Tensor, succ_codebook: torch.Tensor, proj
 
 
 # ---------------------------------------------------------------------------- drafted trees
+#
+# These calls take a few microseconds on the GPU, so their marshalling is kept short: one attribute read per fact,
+# no helper call per tensor, and the raw stream handle where the caller names no stream.
 
 
 def _stream_on(dev: torch.device, stream) -> torch.cuda.Stream:
@@ -593,32 +596,25 @@ def _stream_on(dev: torch.device, stream) -> torch.cuda.Stream:
     return stream
 
 
-class _CallOn:
-    """Runs a call's allocations and launches on its stream and device, whatever the current ones are."""
-
-    def __init__(self, dev: torch.device, stream):
-        self.stream = _stream_on(dev, stream)
-        here = stream is None and torch.cuda.current_device() == dev.index
-        self.guard = None if here else torch.cuda.stream(self.stream)
-
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call_on(dev: torch.device, stream):
+    """(context or None, stream handle): a call's allocations and launches happen on its stream and device,
+    whatever the current ones are. None: they are the current ones."""
+    if stream is None and torch._C._cuda_getDevice() == dev.index:
+        return None, torch._C._cuda_getCurrentRawStream(dev.index)
+    s = _stream_on(dev, stream)
+    return torch.cuda.stream(s), s.cuda_stream
 
 
 _tree_ws = {}
 
 
-def _tree_workspace(op: str, dev: torch.device, stream: int, nbytes: int) -> torch.Tensor:
-    """A zeroed workspace for a call without one: cached per operator, device and stream, so that calls that may
-    overlap never share one. A call that is being captured gets its own, zeroed by the graph."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+def _tree_workspace(op: str, dev: torch.device, stream: int, nbytes: int, zeroed: int) -> torch.Tensor:
+    """A workspace for a call without one, its first `zeroed` bytes zero: cached per operator, device and stream, so
+    that calls that may overlap never share one. A call that is being captured gets its own, zeroed by the graph."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        buf[:zeroed].zero_()
+        return buf
     key = (op, dev.index, stream)
     buf = _tree_ws.get(key)
     if buf is None or buf.numel() < nbytes:
@@ -627,32 +623,32 @@ def _tree_workspace(op: str, dev: torch.device, stream: int, nbytes: int) -> tor
     return buf
 
 
-def _tree_device(**tensors) -> torch.device:
-    """The one CUDA device of the given tensors (None entries apart)."""
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) != 1 or next(iter(devs)).type != "cuda":
-        raise ValueError(f"{', '.join(tensors)} must be on one CUDA device")
-    return next(iter(devs))
+def _bad(name: str, shape, dtype):
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
 
 
-def _expect(name: str, t: Optional[torch.Tensor], shape, dtype) -> None:
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+_I32 = torch.int32
 
 
-def _expect_error_word(t: Optional[torch.Tensor]) -> None:
-    if t is not None and (t.element_size() != 4 or t.dtype.is_floating_point or t.numel() < 1):
-        raise ValueError("device_error must hold a 32-bit integer")
+def _check_i32(t: torch.Tensor, shape, dev: int, name: str) -> int:
+    """The address of a contiguous int32 tensor of `shape` on CUDA device dev."""
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on the CUDA device of the "
+                         "other tensors")
+    return t.data_ptr()
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _check_ws(ws: torch.Tensor, dev: int) -> int:
+    """Bytes of a given workspace."""
+    if not ws.is_contiguous() or ws.get_device() != dev:
+        raise ValueError("workspace must be contiguous, on the CUDA device of the tensors")
+    return ws.numel() * ws.element_size()
 
 
-def _ws_args(ws: torch.Tensor):
-    if not ws.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+def _check_word(t: torch.Tensor, dev: int) -> int:
+    if t.element_size() != 4 or t.dtype.is_floating_point or t.numel() < 1 or t.get_device() != dev:
+        raise ValueError("device_error must hold a 32-bit integer, on the CUDA device of the tensors")
+    return t.data_ptr()
 
 
 def logprobs_workspace_bytes(num_rows: int, vocab: int, top_k: int) -> int:
@@ -661,6 +657,25 @@ def logprobs_workspace_bytes(num_rows: int, vocab: int, top_k: int) -> int:
     if n == 0:
         raise DflashError(ERR_INVALID_ARG, "invalid sizes for the log probability workspace")
     return n
+
+
+def _row_stride(logits: torch.Tensor, rows: int, V: int) -> int:
+    """The one stride of the rows of logits [..., V]."""
+    if V > 1 and logits.stride(-1) != 1:
+        raise ValueError("logits must have a contiguous last dimension")
+    if rows <= 1 or logits.is_contiguous():
+        return V
+    # from the innermost dimension of more than one entry outwards
+    want = row = None
+    for n, st in zip(reversed(logits.shape[:-1]), reversed(logits.stride()[:-1])):
+        if n == 1:
+            continue
+        if row is None:
+            row = st
+        elif st != want:
+            raise ValueError("the rows of logits must have one stride")
+        want = st * n
+    return row
 
 
 def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, top_k: int = 0,
@@ -673,69 +688,85 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     top_tokens int32 [..., top_k] or None, top_logp [..., top_k] or None), float32 unless said. The
     top tokens come largest first, of equal logits the smaller id first: the candidates and unary
     scores of selector_walk. device_error: an optional int32 device word that receives DEVERR_* bits."""
-    lib = load_library()
-    if logits.dim() < 1 or logits.shape[-1] < 1 or (logits.shape[-1] > 1 and logits.stride(-1) != 1):
-        raise ValueError("logits must be [..., V] with a contiguous last dimension")
-    lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
+    lib = _lib or load_library()
+    shape = logits.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("logits must be [..., V]")
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA device")
+    lead, V = shape[:-1], shape[-1]
     R = math.prod(lead)
-    rows = logits.reshape(R, V) if logits.is_contiguous() else logits
-    if rows.dim() != 2:
-        # leading dims of one common row stride
-        for i in range(logits.dim() - 2):
-            if logits.shape[i] > 1 and logits.stride(i) != logits.stride(i + 1) * logits.shape[i + 1]:
-                raise ValueError("the rows of logits must have one stride")
-        stride = logits.stride(-2) if logits.dim() > 1 else V
-    else:
-        stride = rows.stride(0)
-    stride = max(stride, V) if R <= 1 else stride
+    row = _row_stride(logits, R, V)
     code = _dtype_code(logits)
-    m = 0
+    dev, index = logits.device, logits.get_device()
+    m, tok = 0, None
     if tokens is not None:
-        if tokens.dim() != len(lead) + 1:
-            raise ValueError("tokens must be int32 [..., m] with the leading dims of logits")
-        m = tokens.shape[-1]
-        _expect("tokens", tokens, lead + (m,), torch.int32)
-    _expect_error_word(device_error)
-    dev = _tree_device(logits=logits, tokens=tokens, device_error=device_error, workspace=workspace)
-    with _CallOn(dev, stream) as handle:
-        f32 = dict(dtype=torch.float32, device=dev)
-        log_z = torch.empty(lead, **f32)
-        entropy = torch.empty(lead, **f32) if want_entropy else None
-        token_logp = torch.empty(lead + (m,), **f32) if tokens is not None else None
-        top_tokens = torch.empty(lead + (top_k,), dtype=torch.int32, device=dev) if top_k > 0 else None
-        top_logp = torch.empty(lead + (top_k,), **f32) if top_k > 0 else None
+        m = tokens.shape[-1] if tokens.dim() == len(shape) else -1
+        tok = _check_i32(tokens, lead + (m,), index, "tokens") if m else None
+        if m <= 0 and tuple(tokens.shape) != tuple(lead) + (0,):
+            _bad("tokens", lead + ("m",), "torch.int32")
+    word = None if device_error is None else _check_word(device_error, index)
+    given_bytes = None if workspace is None else _check_ws(workspace, index)
+    ctx, handle = _call_on(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        log_z = torch.empty(lead, dtype=torch.float32, device=dev)
+        entropy = token_logp = top_tokens = top_logp = None
+        if want_entropy:
+            entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+        if tokens is not None:
+            token_logp = torch.empty(lead + (m,), dtype=torch.float32, device=dev)
+        if top_k > 0:
+            top_tokens = torch.empty(lead + (top_k,), dtype=_I32, device=dev)
+            top_logp = torch.empty(lead + (top_k,), dtype=torch.float32, device=dev)
         if workspace is None and R > 0:
-            workspace = _tree_workspace("token_logprobs", dev, handle, logprobs_workspace_bytes(R, V, top_k))
-        ws, ws_bytes = _ws_args(workspace) if workspace is not None else (None, 0)
-        _check(lib.dflash_token_logprobs(_ptr(logits), code, R, V, stride, float(temperature),
-                                         _ptr(tokens) if m else None, m, _ptr(token_logp) if m else None, _ptr(log_z),
-                                         _ptr(entropy), int(top_k), _ptr(top_tokens), _ptr(top_logp),
-                                         _ptr(device_error), ws, ws_bytes, handle))
+            given_bytes = lib.dflash_logprobs_workspace_bytes(R, V, top_k)
+            # (0 for sizes that the call itself refuses with the reason)
+            workspace = _tree_workspace("token_logprobs", dev, handle, given_bytes, 4 * R) if given_bytes else None
+        st = lib.dflash_token_logprobs(
+            logits.data_ptr(), code, R, V, row, temperature, tok, m, token_logp.data_ptr() if m else None,
+            log_z.data_ptr(), entropy.data_ptr() if want_entropy else None, top_k,
+            top_tokens.data_ptr() if top_k > 0 else None, top_logp.data_ptr() if top_k > 0 else None, word,
+            None if workspace is None else workspace.data_ptr(), given_bytes or 0, handle)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if st:
+        _check(st)
     return token_logp, entropy, log_z, top_tokens, top_logp
 
 
-def _tree_cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
-                     first: int) -> Dims:
-    """Dims of a cache [..., num_pages, page_size, Hkv, D] whose page dimension is `first`, and its requests."""
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride() or v_cache.dtype != k_cache.dtype:
+_tree_dims = {}  # (layout of a call) -> (its Dims, their address for ctypes, workspace bytes)
+
+
+def _tree_cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, first: int, hq: int,
+                     max_seq_len: Optional[int], T: int):
+    """(Dims, byref, tree attention's workspace bytes) of a cache [..., num_pages, page_size, Hkv, D] whose page
+    dimension is `first`. Only sizes and strides decide them, so they are made once per layout."""
+    shape, strides, dtype, table = k_cache.shape, k_cache.stride(), k_cache.dtype, page_table.shape
+    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype is not dtype:
         raise ValueError("v_cache must match k_cache in shape, strides and dtype")
-    if k_cache.stride(-1) != 1:
-        raise ValueError("the caches' head_dim must be contiguous")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor")
-    B = page_table.shape[0]
-    _expect("page_table", page_table, page_table.shape, torch.int32)
-    _expect("seq_lens", seq_lens, (B,), torch.int32)
-    d = Dims()
-    d.batch = B
-    d.num_q_heads = d.num_kv_heads = k_cache.shape[first + 2]
-    d.head_dim = k_cache.shape[first + 3]
-    d.page_size = k_cache.shape[first + 1]
-    d.num_pages = k_cache.shape[first]
-    d.max_pages = page_table.shape[1]
-    d.dtype = _dtype_code(k_cache)
-    d.kv_stride_page, d.kv_stride_slot, d.kv_stride_head = (int(s) for s in k_cache.stride()[first:first + 3])
-    return d
+    key = (shape, strides, dtype, table, first, hq, max_seq_len, T, k_cache.get_device())
+    hit = _tree_dims.get(key)
+    if hit is None:
+        if strides[-1] != 1:
+            raise ValueError("the caches' head_dim must be contiguous")
+        d = Dims()
+        d.batch, d.max_pages = table
+        d.num_kv_heads, d.head_dim = shape[first + 2], shape[first + 3]
+        d.num_q_heads = hq or d.num_kv_heads
+        d.page_size, d.num_pages = shape[first + 1], shape[first]
+        d.max_seq_len = int(max_seq_len) if max_seq_len else 0
+        d.dtype = _dtype_code(k_cache)
+        d.kv_stride_page, d.kv_stride_slot, d.kv_stride_head = (int(s) for s in strides[first:first + 3])
+        with torch.cuda.device(k_cache.device):
+            nbytes = load_library().dflash_tree_attn_workspace_bytes(ctypes.byref(d), T) if hq else 0
+        hit = (d, ctypes.byref(d), nbytes)
+        if len(_tree_dims) > 256:
+            _tree_dims.clear()
+        _tree_dims[key] = hit
+    return hit
 
 
 def tree_attn_workspace_bytes(dims: Dims, max_nodes: int) -> int:
@@ -761,49 +792,66 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     (out [B*T, Hq, D] in q's dtype, lse fp32 [B*T, Hq] or None); padding rows of given outputs keep
     what they held, those of new ones are zero. Without a workspace the call uses one of its stream's (or the
     captured graph's); its error word is read with tree_attn_error()."""
-    lib = load_library()
-    if q.dim() != 3 or k_cache.dim() != 4 or parents.dim() != 2:
+    lib = _lib or load_library()
+    qs, ps = q.shape, parents.shape
+    if len(qs) != 3 or k_cache.dim() != 4 or len(ps) != 2:
         raise ValueError("q must be [B*T, Hq, D], the caches [num_pages, page_size, Hkv, D] and parents [B, T]")
-    B, T = parents.shape
-    _expect("q", q, (B * T, q.shape[1], k_cache.shape[3]), k_cache.dtype)
-    dims = _tree_cache_dims(k_cache, v_cache, page_table, seq_lens, 0)
-    dims.num_q_heads = q.shape[1]
-    dims.max_seq_len = int(max_seq_len) if max_seq_len else 0
-    _expect("seq_lens", seq_lens, (B,), torch.int32)
-    _expect("parents", parents, (B, T), torch.int32)
-    _expect("num_nodes", num_nodes, (B,), torch.int32)
-    _expect("out", out, q.shape, q.dtype)
-    _expect("lse", lse, q.shape[:2], torch.float32)
     if kernel not in ("auto", "simt", "tc"):
         raise ValueError("kernel must be 'auto', 'simt' or 'tc'")
-    if scale is None:
-        scale = 1.0 / math.sqrt(q.shape[2])
-    dev = _tree_device(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seq_lens=seq_lens,
-                       parents=parents, num_nodes=num_nodes, out=out, lse=lse, workspace=workspace)
-    with _CallOn(dev, stream) as handle:
+    B, T = ps
+    dev, index = q.device, q.get_device()
+    if q.dtype is not k_cache.dtype or qs != (B * T, qs[1], k_cache.shape[3]) or not q.is_contiguous():
+        _bad("q", (B * T, qs[1], k_cache.shape[3]), k_cache.dtype)
+    if index < 0 or k_cache.get_device() != index or v_cache.get_device() != index:
+        raise ValueError("q and the caches must be on one CUDA device")
+    batch = (B,)
+    table_at = _check_i32(page_table, (B, page_table.shape[-1]), index, "page_table")
+    lens_at = _check_i32(seq_lens, batch, index, "seq_lens")
+    parents_at = _check_i32(parents, ps, index, "parents")
+    nodes_at = None if num_nodes is None else _check_i32(num_nodes, batch, index, "num_nodes")
+    if out is not None and (out.dtype is not q.dtype or out.shape != qs or not out.is_contiguous()
+                            or out.get_device() != index):
+        _bad("out", qs, q.dtype)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != qs[:2] or not lse.is_contiguous()
+                            or lse.get_device() != index):
+        _bad("lse", qs[:2], torch.float32)
+    dims, dims_ref, nbytes = _tree_cache_dims(k_cache, v_cache, page_table, 0, qs[1], max_seq_len, T)
+    if workspace is not None:
+        nbytes = _check_ws(workspace, index)
+    ctx, handle = _call_on(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         fresh = torch.empty if num_nodes is None else torch.zeros
-        if workspace is None:
-            workspace = _tree_workspace("tree_attn", dev, handle, tree_attn_workspace_bytes(dims, T))
-        ws, ws_bytes = _ws_args(workspace)
+        if workspace is None and nbytes:  # (0: sizes that the call itself refuses with the reason)
+            workspace = _tree_workspace("tree_attn", dev, handle, nbytes, 256)
         if out is None:
-            out = fresh(q.shape, dtype=q.dtype, device=dev)
+            out = fresh(qs, dtype=q.dtype, device=dev)
         if lse is None and want_lse:
-            lse = fresh(q.shape[:2], dtype=torch.float32, device=dev)
-        _check(lib.dflash_tree_attn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
-                                    _ptr(parents), _ptr(num_nodes), ctypes.byref(dims), T, int(window), float(scale),
-                                    _ptr(out), _ptr(lse), KERNELS[kernel], ws, ws_bytes, int(wait_limit_us), handle))
+            lse = fresh(qs[:2], dtype=torch.float32, device=dev)
+        st = lib.dflash_tree_attn(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, parents_at, nodes_at, dims_ref, T, window,
+            1.0 / math.sqrt(qs[2]) if scale is None else scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), KERNELS[kernel],
+            None if workspace is None else workspace.data_ptr(), nbytes, wait_limit_us, handle)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if st:
+        _check(st)
     return out, lse
 
 
 def tree_attn_error(device=None, stream=None, clear: bool = True) -> int:
     """The error word (DEVERR_* bits) of the workspace that tree_attn calls without one share on a stream;
     synchronises the stream."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    dev = torch.device("cuda" if device is None else device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    with _CallOn(dev, stream) as handle:
-        ws = _tree_ws.get(("tree_attn", dev.index, handle))
-        return 0 if ws is None else read_error(ws, clear=clear, stream=handle)
+    s = _stream_on(dev, stream)
+    with torch.cuda.stream(s):
+        ws = _tree_ws.get(("tree_attn", dev.index, s.cuda_stream))
+        return 0 if ws is None else read_error(ws, clear=clear, stream=s)
 
 
 def tree_accept(logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor,
@@ -814,31 +862,51 @@ def tree_accept(logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tenso
     stride, last dim contiguous), tokens and parents int32 [B, T], num_nodes int32 [B] or None. Returns
     (accepted_len [B], path [B, T], next_token [B], target argmax [B, T] or None), int32: path holds the
     accepted nodes from the root on, -1 behind them."""
-    lib = load_library()
-    if logits.dim() != 3 or logits.shape[2] < 1 or (logits.shape[2] > 1 and logits.stride(2) != 1):
-        raise ValueError("logits must be [B, T, V] with a contiguous last dimension")
-    B, T, V = logits.shape
-    row = logits.stride(1) if T > 1 else logits.stride(0) if B > 1 else V
-    if B > 1 and T > 1 and logits.stride(0) != T * row:
-        raise ValueError("the rows of logits must have one stride")
+    lib = _lib or load_library()
+    shape = logits.shape
+    if len(shape) != 3 or shape[2] < 1:
+        raise ValueError("logits must be [B, T, V]")
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA device")
+    B, T, V = shape
+    row = _row_stride(logits, B * T, V)
     code = _dtype_code(logits)
-    _expect("tokens", tokens, (B, T), torch.int32)
-    _expect("parents", parents, (B, T), torch.int32)
-    _expect("num_nodes", num_nodes, (B,), torch.int32)
-    _expect_error_word(device_error)
-    dev = _tree_device(logits=logits, tokens=tokens, parents=parents, num_nodes=num_nodes, device_error=device_error,
-                       workspace=workspace)
-    with _CallOn(dev, stream) as handle:
-        i32 = dict(dtype=torch.int32, device=dev)
-        accepted, path, nxt = torch.empty(B, **i32), torch.empty((B, T), **i32), torch.empty(B, **i32)
-        argmax = torch.empty((B, T), **i32) if want_argmax else None
+    dev, index = logits.device, logits.get_device()
+    rows, batch = shape[:2], (B,)
+    tokens_at = _check_i32(tokens, rows, index, "tokens")
+    parents_at = _check_i32(parents, rows, index, "parents")
+    nodes_at = None if num_nodes is None else _check_i32(num_nodes, batch, index, "num_nodes")
+    word = None if device_error is None else _check_word(device_error, index)
+    nbytes = _accept_bytes(lib) if workspace is None else _check_ws(workspace, index)
+    ctx, handle = _call_on(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        accepted = torch.empty(batch, dtype=_I32, device=dev)
+        nxt = torch.empty(batch, dtype=_I32, device=dev)
+        path = torch.empty(rows, dtype=_I32, device=dev)
+        argmax = torch.empty(rows, dtype=_I32, device=dev) if want_argmax else None
         if workspace is None:
-            workspace = _tree_workspace("tree_accept", dev, handle, lib.dflash_tree_accept_workspace_bytes())
-        ws, ws_bytes = _ws_args(workspace)
-        _check(lib.dflash_tree_accept(_ptr(logits), code, B, T, V, row, _ptr(tokens), _ptr(parents), _ptr(num_nodes),
-                                      _ptr(accepted), _ptr(path), _ptr(nxt), _ptr(argmax), _ptr(device_error), ws,
-                                      ws_bytes, handle))
+            workspace = _tree_workspace("tree_accept", dev, handle, nbytes, nbytes)
+        st = lib.dflash_tree_accept(
+            logits.data_ptr(), code, B, T, V, row, tokens_at, parents_at, nodes_at, accepted.data_ptr(), path.data_ptr(), nxt.data_ptr(),
+            argmax.data_ptr() if want_argmax else None, word, workspace.data_ptr(), nbytes, handle)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if st:
+        _check(st)
     return accepted, path, nxt, argmax
+
+
+_accept_ws_bytes = 0
+
+
+def _accept_bytes(lib) -> int:
+    global _accept_ws_bytes
+    if not _accept_ws_bytes:
+        _accept_ws_bytes = lib.dflash_tree_accept_workspace_bytes()
+    return _accept_ws_bytes
 
 
 def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -849,28 +917,39 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.
     [num_pages, page_size, Hkv, D], or [layers, num_pages, page_size, Hkv, D] for every layer at once; path
     int32 [B, T] and accepted_len int32 [B] of tree_accept; seq_lens int32 [B] (context + nodes).
     Returns new_lens int32 [B] (context + bonus token + accepted tokens), which may be seq_lens itself."""
-    lib = load_library()
-    if k_cache.dim() not in (4, 5) or path.dim() != 2:
-        raise ValueError("the caches must be [(layers,) num_pages, page_size, Hkv, D] and path [B, T]")
+    lib = _lib or load_library()
     first = k_cache.dim() - 4
-    dims = _tree_cache_dims(k_cache, v_cache, page_table, seq_lens, first)
-    dims.max_seq_len = int(max_seq_len) if max_seq_len else 0
-    B, T = path.shape
-    _expect("seq_lens", seq_lens, (B,), torch.int32)
-    _expect("path", path, (B, T), torch.int32)
-    _expect("accepted_len", accepted_len, (B,), torch.int32)
-    _expect("num_nodes", num_nodes, (B,), torch.int32)
-    _expect("new_lens", new_lens, (B,), torch.int32)
-    _expect_error_word(device_error)
-    dev = _tree_device(k_cache=k_cache, v_cache=v_cache, page_table=page_table, seq_lens=seq_lens, path=path,
-                       accepted_len=accepted_len, num_nodes=num_nodes, new_lens=new_lens, device_error=device_error)
-    with _CallOn(dev, stream) as handle:
+    shape = path.shape
+    if first not in (0, 1) or len(shape) != 2:
+        raise ValueError("the caches must be [(layers,) num_pages, page_size, Hkv, D] and path [B, T]")
+    B, T = shape
+    dev, index = k_cache.device, k_cache.get_device()
+    if index < 0 or v_cache.get_device() != index:
+        raise ValueError("the caches must be on one CUDA device")
+    batch = (B,)
+    table_at = _check_i32(page_table, (B, page_table.shape[-1]), index, "page_table")
+    lens_at = _check_i32(seq_lens, batch, index, "seq_lens")
+    path_at = _check_i32(path, shape, index, "path")
+    accepted_at = _check_i32(accepted_len, batch, index, "accepted_len")
+    nodes_at = None if num_nodes is None else _check_i32(num_nodes, batch, index, "num_nodes")
+    if new_lens is not None:
+        _check_i32(new_lens, batch, index, "new_lens")
+    dims, dims_ref, _ = _tree_cache_dims(k_cache, v_cache, page_table, first, 0, max_seq_len, T)
+    word = None if device_error is None else _check_word(device_error, index)
+    ctx, handle = _call_on(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        _check(lib.dflash_tree_commit(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(path),
-                                      _ptr(accepted_len), _ptr(num_nodes), _ptr(new_lens), ctypes.byref(dims), T,
-                                      k_cache.shape[0] if first else 1, k_cache.stride(0) if first else 0,
-                                      _ptr(device_error), handle))
+            new_lens = torch.empty(batch, dtype=_I32, device=dev)
+        st = lib.dflash_tree_commit(
+            k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, path_at, accepted_at, nodes_at,
+            new_lens.data_ptr(), dims_ref, T, k_cache.shape[0] if first else 1, k_cache.stride(0) if first else 0, word, handle)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if st:
+        _check(st)
     return new_lens
 
 

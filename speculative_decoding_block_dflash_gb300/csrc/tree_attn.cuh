@@ -65,16 +65,22 @@ __device__ __forceinline__ int32_t ranges_used(const TreeAttnParams& p, int64_t 
     return (int32_t)(total < p.ranges ? total : p.ranges);
 }
 
+// a / b for a >= 0, b > 0; the 64-bit division is a long routine, and the numbers are mostly small.
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b)
+{
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Where range r begins when a weight of `total` is dealt to `ranges` ranges.
 __device__ __forceinline__ int64_t range_begin(int64_t total, int32_t ranges, int32_t r)
 {
-    return total * r / ranges;
+    return div_small(total * r, ranges);
 }
 
 // The range that holds unit x of the weight.
 __device__ __forceinline__ int32_t range_of(int64_t total, int32_t ranges, int64_t x)
 {
-    int32_t r = (int32_t)(x * ranges / total);
+    int32_t r = (int32_t)div_small(x * ranges, total);
     while (r + 1 < ranges && range_begin(total, ranges, r + 1) <= x) ++r;
     while (r > 0 && range_begin(total, ranges, r) > x) --r;
     return r;
@@ -100,21 +106,27 @@ struct PieceWalk {
     __device__ __forceinline__ void start(const TreeAttnParams& p, int32_t r)
     {
         const int lane = threadIdx.x & 31;
-        const int64_t total = tree_weight_before(p, p.B);
+        b = g = at = t0 = t1 = 0;
+        left = 0;
+        req.n = req.ctx = req.L = req.lo = req.tile0 = req.nt = 0;
+        req.bad = false;
+        // the first 32 requests, a lane each: all there are, mostly
+        const TreeReq own = lane < p.B ? tree_request(p, lane) : req;
+        int64_t mine = tree_weight(own) * p.Hkv;
+        int64_t total = mine;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+        if (p.B > 32) total = tree_weight_before(p, p.B);
         const int32_t used = ranges_used(p, total);
         int64_t x = 0;
-        left = 0;
         if (r < used) {
             x = range_begin(total, used, r);
             left = range_begin(total, used, r + 1) - x;
         }
-        b = g = at = t0 = t1 = 0;
-        req.n = req.ctx = req.L = req.lo = req.tile0 = req.nt = 0;
-        req.bad = false;
         if (left <= 0) return;
 #pragma unroll 1
-        for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
-            const int64_t mine = b0 + lane < p.B ? tree_weight(tree_request(p, b0 + lane)) * p.Hkv : 0;
+        for (int32_t b0 = 0;; b0 += 32) {
+            if (b0 > 0) mine = b0 + lane < p.B ? tree_weight(tree_request(p, b0 + lane)) * p.Hkv : 0;
             int64_t incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -129,10 +141,23 @@ struct PieceWalk {
                 break;
             }
             x -= __shfl_sync(0xffffffffu, incl, 31);
+            if (b0 + 32 >= p.B) {  // not reached: x lies below the total
+                left = 0;
+                return;
+            }
         }
-        req = tree_request(p, b);
-        g = (int32_t)(x / tree_weight(req));
-        at = (int32_t)(x - (int64_t)g * tree_weight(req));
+        if (b < 32) {
+            req.n = __shfl_sync(0xffffffffu, own.n, b);
+            req.L = __shfl_sync(0xffffffffu, own.L, b);
+            req.ctx = __shfl_sync(0xffffffffu, own.ctx, b);
+            req.lo = __shfl_sync(0xffffffffu, own.lo, b);
+            req.tile0 = __shfl_sync(0xffffffffu, own.tile0, b);
+            req.nt = __shfl_sync(0xffffffffu, own.nt, b);
+        } else {
+            req = tree_request(p, b);
+        }
+        g = (int32_t)div_small(x, tree_weight(req));
+        at = (int32_t)(x - g * tree_weight(req));
         cut();
         if (done()) next(p);  // the range begins in a pair's first units and ends there, or it does not reach a tile
     }

@@ -250,14 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&ms.tmem, 512);
         tmem_relinquish();
     }
+    PieceWalk w;
+    w.start(p, range);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     cudaTriggerProgrammaticLaunchCompletion();  // the join grid may take its place; it waits for this one to end
     const uint32_t tmem = ms.tmem;
-
-    PieceWalk w;
-    w.start(p, range);
     bool ok = true;
     auto live_rows = [&]() -> int32_t { return min(p.npt, w.req.n - node0) * p.Gc; };  // <= 0: nothing for this CTA
 
@@ -412,7 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     qd += q_chunk;
                     at.advance(1, S);
                 }
-                if (ok && elect_one()) tc_commit(ms.s_full + (t & 1));
+                if (ok && elect_one()) {
+                    tc_commit(ms.s_full + (t & 1));
+                }
                 __syncwarp();
                 return at;
             };

@@ -9,7 +9,7 @@ namespace dflash {
 // One dflash_tree_attn call, validated on the host.
 //
 // Work. A query tile is the rows of npt nodes x Gc heads of one KV head (row = node * Gc + head, `rows` of
-// them); a request has n_sub = (G / Gc) * ceil(T / npt) * ndv of them per KV head, ndv being the slices of the
+// them); a request has n_sub = (G / Gc) * nrt * ndv of them, nrt being the node tiles, per KV head, ndv being the slices of the
 // value's dims that one CTA's accumulators hold. Every one of them reads the same K/V, so the key tiles of
 // all (request, KV head) pairs, laid end to end, are cut into `ranges` equal ranges and a CTA
 // takes (range, query tile): each range is streamed by the n_sub CTAs of consecutive block
@@ -36,7 +36,8 @@ struct TreeAttnParams {
     int32_t window;
     float scale;
     int32_t dtype;
-    int32_t Gc, npt, ndv, rows, DV, n_sub, ranges;
+    int32_t Gc, npt, nrt, ndv, rows, DV, n_sub, ranges;
+    int32_t pair;  // 1: tensor-core CTA pairs; neighbouring node tiles are neighbouring query tiles
     int32_t tile;  // keys per tile
     unsigned long long wait_ns;
 };
@@ -45,7 +46,7 @@ struct TreeAttnParams {
 void tree_attn_plan(TreeAttnParams& p, int kernel);
 bool tree_tc_supports(const dflash_dims* d);
 cudaError_t launch_tree_attn_simt(const TreeAttnParams& p, cudaStream_t stream);
-cudaError_t launch_tree_attn_tc(const TreeAttnParams& p, cudaStream_t stream);
+cudaError_t launch_tree_attn_tc(TreeAttnParams& p, cudaStream_t stream);  // may take fewer ranges than planned
 cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream);
 
 // Log probabilities (csrc/token_logprobs.cu).

@@ -77,8 +77,7 @@ void fill_sizes(TreeAttnParams& p, const dflash_dims* d, int32_t T)
 void tree_attn_plan(TreeAttnParams& p, int kernel)
 {
     const bool tc = kernel == DFLASH_KERNEL_TC;
-    // rows of a query tile: two tensor-core tiles of 128 where their accumulators fit TMEM (head_dim <= 128)
-    const int32_t most = tc ? (p.D <= 128 ? 256 : 128) : 64;
+    const int32_t most = tc ? 128 : 64;  // rows of a query tile
     p.Gc = 1;
     for (int32_t gc = std::min(p.G, most); gc >= 1; --gc)
         if (p.G % gc == 0) {
@@ -86,13 +85,16 @@ void tree_attn_plan(TreeAttnParams& p, int kernel)
             break;
         }
     const int32_t fit = most / p.Gc;
-    const int32_t nrt = (p.T + fit - 1) / fit;
-    p.npt = (p.T + nrt - 1) / nrt;  // node tiles of equal size
+    p.nrt = (p.T + fit - 1) / fit;
+    // several node tiles on the tensor cores: CTA pairs, an even number of tiles
+    p.pair = tc && p.nrt > 1 ? 1 : 0;
+    if (p.pair) p.nrt = (p.nrt + 1) / 2 * 2;
+    p.npt = (p.T + p.nrt - 1) / p.nrt;  // node tiles of equal size
     p.rows = p.npt * p.Gc;
     p.tile = tc ? 128 : 64;
-    p.DV = !tc ? p.D : p.D <= 64 ? 64 : p.D <= 128 ? 128 : 256;
+    p.DV = !tc ? p.D : p.D <= 64 && !p.pair ? 64 : p.D <= 128 ? 128 : 256;
     p.ndv = (p.D + p.DV - 1) / p.DV;
-    p.n_sub = (p.G / p.Gc) * ((p.T + p.npt - 1) / p.npt) * p.ndv;
+    p.n_sub = (p.G / p.Gc) * p.nrt * p.ndv;
     // one wave: the tensor-core kernel and the wide SIMT tiles hold one CTA per SM, the SIMT kernel at head_dim 64 two
     const int32_t ctas = device_sm_count() * (!tc && p.D <= 64 ? 2 : 1);
     p.ranges = std::max(1, ctas / p.n_sub);

@@ -191,11 +191,14 @@ struct SubTile {
 __device__ __forceinline__ SubTile sub_tile(const TreeAttnParams& p, int32_t sub)
 {
     SubTile s;
+    const int32_t odd = p.pair ? sub & 1 : 0;
+    if (p.pair) sub >>= 1;
+    const int32_t tiles = p.pair ? p.nrt / 2 : p.nrt;
     s.dv = sub % p.ndv;
     const int32_t rest = sub / p.ndv;
-    const int32_t nrt = (p.T + p.npt - 1) / p.npt;
-    s.rt = rest % nrt;
-    s.gc = rest / nrt;
+    s.rt = rest % tiles;
+    if (p.pair) s.rt = 2 * s.rt + odd;
+    s.gc = rest / tiles;
     return s;
 }
 

@@ -9,16 +9,22 @@
 // neither shared memory nor TMEM, and shared memory is left to Q and the ring: what bounds the kernel is
 // the K/V stream, whose rate is the bytes in flight over the latency.
 //
-// TMEM (512 columns): S0, S1 (128 each) and 256 columns of O. The two S buffers are used in one of three
-// ways, t counting the steps of a piece (one range's part of a request and KV head):
-//   two row tiles (DV <= 128, more than 128 rows): step t = tile t / 2, row tile t % 2, with its own O; every
-//     K/V byte serves 256 rows;
-//   one row tile, DV <= 128: step t = tile t, its O the one of t % 2: two warpgroups take alternate tiles
-//     with a maximum, a sum and an O each, joined when the piece ends, so neither waits for the other;
-//   one row tile, DV = 256: step t = tile t, one O, one warpgroup; S(t+1) is computed while the
-//     softmax of S(t) runs. For head_dim above 256 a CTA computes 256 of the output's dims from the whole S.
-// In all three the MMA warp does: S(0), S(1), then for every t: O += P(t) V, S(t + 2), which reuses
-// the buffer of P(t) (MMAs of one thread execute in order).
+// TMEM (512 columns): S0, S1 (128 each) and 256 columns of O. A query tile is up to 128 rows; step t of a piece (one
+// range's part of a request and KV head) is its key tile t, with S buffer t % 2:
+//   DV <= 128: two O accumulators, of even and odd steps: two warpgroups take alternate tiles with a maximum, a sum and an
+//     O each, joined when the piece ends, so neither waits for the other;
+//   DV = 256: one O, one warpgroup; S(t+1) is computed while the softmax of S(t) runs. For head_dim above 256 a CTA
+//     computes 256 of the output's dims from the whole S.
+// The MMA warp does: S(0), S(1), then for every t: O += P(t) V, S(t + 2), which reuses the buffer of P(t) (MMAs of one
+// thread execute in order).
+//
+// More than 128 rows per KV head: CTA pairs (clusters of two, cta_group::2). The two CTAs hold neighbouring query tiles and
+// share every MMA (M = 256): each loads half of the K tile's keys and half of the V tile's dims, so a K/V byte
+// enters one SM for 256 rows, and an SM reads half of each B operand from its shared memory, which is what bounds an
+// MMA of 128 x 128 x 16 (97 cycles measured with both operands in one SM's shared memory, against 64 at the tensor
+// peak). The even CTA's thread issues; its commits arrive in both CTAs; softmax warps of both arrive at the even
+// CTA's barriers. (Two tiles of 128 rows in one CTA instead took 177 us for the ragged batch of 64-node trees, 2.6 us
+// a tile of 128 keys, of which the MMAs were 1.5.)
 //
 // Online softmax about a lazy maximum: a row's maximum moves only when a score exceeds it by 2^8 in the exp2 domain; O
 // and the sum are then rescaled in place. P <= 2^8 in bf16 rounds each probability to 2^-8 relative, the same choice the
@@ -30,8 +36,9 @@
 // reach every row.
 //
 // Warps: 0-3 and 4-7 softmax and output, 8-10 TMA producers, 11 the MMA issuer. Ring stages are 16 KB: K 128 keys
-// x 64 dims; V 64 keys x 128 dims (128 keys x 64 dims at DV = 64). A box is 64 dims of up to 64 tokens of
-// one page; its id is read one stage ahead by the lane that issues it. Boxes past the keys or before the window are
+// x 64 dims, V 64 keys x 128 dims (128 keys x 64 dims at DV = 64); in a pair each CTA's halves are K 64 keys x
+// 128 dims, V 64 keys x 128 dims (DV = 256) or 128 keys x 64 dims. A box is 64 dims of up to 64 tokens of one page; its
+// id is read one stage ahead by the lane that issues it. Boxes past the keys or before the window are
 // fetched at an out-of-bounds page, which the TMA unit fills with zeros without a look at the table.
 //
 // Every mbarrier wait is bounded (p.wait_ns): on expiry the kernel records DFLASH_DEVERR_TIMEOUT, waits (bounded) for its
@@ -58,6 +65,7 @@ constexpr int kStageBytes = 16384;
 constexpr int kMaxStages = 13;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kOCol = 256;  // first TMEM column of O
+constexpr unsigned long long kCopyGraceNs = 200000ull;  // after a failed wait: time for copies in flight to land
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThresh = 8.0f;
@@ -73,6 +81,7 @@ struct TcMisc {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_free;
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+    uint64_t v_clean[kMaxStages];  // pair: the odd CTA has zeroed its rows of the slot's V stage
     uint64_t drain;
     uint32_t tmem;
     int32_t abort;
@@ -143,6 +152,22 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
+__device__ __forceinline__ void tc_mma2_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
+        : "memory");
+}
+
+// Arrives on a barrier of another CTA of the cluster.
+__device__ __forceinline__ void arrive_peer(uint32_t bar_cluster)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // One thread of the warp, always the same.
 __device__ __forceinline__ bool elect_one()
 {
@@ -169,28 +194,18 @@ struct RingPos {
     }
 };
 
-// What ring stage i of a piece of n tiles holds. One row tile: K0 K1 V0 K2 V1 ... V(n-1); two: K0 V0 K1 V1 ...
+// What ring stage i of a piece of n tiles holds: K0 K1 V0 K2 V1 ... V(n-1), ks stages of a K tile and vs of a V tile.
 struct StageOf {
     bool is_k;
     int32_t tile, sub;
 };
 
-__device__ __forceinline__ StageOf stage_of(int32_t i, int32_t n, bool two, int32_t kc, int32_t vs)
+__device__ __forceinline__ StageOf stage_of(int32_t i, int32_t n, int32_t ks, int32_t vs)
 {
-    StageOf s;
-    if (two) {
-        const int32_t j = i / (kc + vs), r = i - j * (kc + vs);
-        s.is_k = r < kc;
-        s.tile = j;
-        s.sub = s.is_k ? r : r - kc;
-        return s;
-    }
-    if (i < kc) return StageOf{true, 0, i};
-    const int32_t j = (i - kc) / (kc + vs), r = i - kc - j * (kc + vs);
-    s.is_k = j < n - 1 && r < kc;
-    s.tile = s.is_k ? j + 1 : j;
-    s.sub = s.is_k || j == n - 1 ? r : r - kc;
-    return s;
+    if (i < ks) return StageOf{true, 0, i};
+    const int32_t j = (i - ks) / (ks + vs), r = i - ks - j * (ks + vs);
+    const bool is_k = j < n - 1 && r < ks;
+    return StageOf{is_k, is_k ? j + 1 : j, is_k || j == n - 1 ? r : r - ks};
 }
 
 // Bits a .. b - 1 of a word (a and b outside [0, 32] are taken to its ends).
@@ -202,14 +217,16 @@ __device__ __forceinline__ uint32_t bit_span(int32_t a, int32_t b)
     return (b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-template <int DV>
+template <int DV, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const TreeAttnParams p, const TcShape x)
 {
-    constexpr bool kAlternate = DV <= 128;        // two O accumulators
-    constexpr int kVN = DV == 64 ? 64 : 128;      // dims of a V stage
-    constexpr int kVKeys = DV == 64 ? 128 : 64;   // and its keys
+    static_assert(DV == 256 || DV == 128 || (DV == 64 && !kPair), "64 dims in halves of 32 have no 128-byte rows");
+    constexpr bool kAlternate = DV <= 128;                            // two O accumulators
+    constexpr int kVN = kPair ? DV : DV == 64 ? 64 : 128;             // dims of a V stage (both CTAs' of a pair)
+    constexpr int kVKeys = kPair ? (DV == 256 ? 64 : 128) : DV == 64 ? 128 : 64;  // and its keys
+    constexpr int kM = kPair ? 256 : 128;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -222,24 +239,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &ms.abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
     const int32_t range = blockIdx.x / p.n_sub, sub = blockIdx.x % p.n_sub;
     const SubTile st = sub_tile(p, sub);
     const int32_t node0 = st.rt * p.npt;
-    const int32_t vc_n = (min(DV, p.D - st.dv * DV) + kVN - 1) / kVN;  // V column groups
-    const int32_t vs_n = (kTile / kVKeys) * vc_n;                       // V stages per tile
+    const int32_t lead0 = (st.rt - (int32_t)rank) * p.npt;  // the even CTA's first node
+    const int32_t ks_n = kPair ? (kc_n + 1) / 2 : kc_n;     // K stages per tile
+    const int32_t vc_n = kPair ? 1 : (min(DV, p.D - st.dv * DV) + kVN - 1) / kVN;  // V column groups
+    const int32_t vs_n = (kTile / kVKeys) * vc_n;                                   // V stages per tile
     const int S = x.stages;
+
+    // What the barriers hand over lies in TMEM (ordered by the tcgen05 fences) or came by the async proxy: waits and
+    // arrivals need no cluster-scope ordering of ordinary memory, which cost a softmax warp about 1 us per arrival.
+    auto bounded_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return ring_wait(bar, parity, abort_flag, p.err, p.wait_ns);
+    };
+    // the even CTA's copy of a barrier
+    auto lead_bar = [&](uint64_t* bar) -> uint32_t { return mapa_shared(smem_u32(bar), 0); };
+    auto commit = [&](uint64_t* bar) {
+        if (kPair)
+            tc_commit2_both(bar);
+        else
+            tc_commit(bar);
+    };
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(ms.full + i, 1);
             mbar_init(ms.empty + i, 1);
+            mbar_init(ms.v_clean + i, 1);
         }
         mbar_init(&ms.q_full, 1);
         mbar_init(&ms.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(ms.s_full + i, 1);
-            mbar_init(ms.p_half + i, 128);
-            mbar_init(ms.p_full + i, 128);
+            mbar_init(ms.p_half + i, kPair ? 8 : 4);  // a softmax warp each
+            mbar_init(ms.p_full + i, kPair ? 8 : 4);
             mbar_init(ms.o_done + i, 1);
         }
         mbar_init(&ms.drain, 1);
@@ -247,47 +283,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(&ms.tmem, 512);
-        tmem_relinquish();
+        if (kPair) {
+            tmem_alloc2(&ms.tmem, 512);
+            tmem_relinquish2();
+        } else {
+            tmem_alloc(&ms.tmem, 512);
+            tmem_relinquish();
+        }
     }
     PieceWalk w;
     w.start(p, range);
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync_all();  // the peer's barriers are set up before anything arrives there
     tc_fence_after();
     cudaTriggerProgrammaticLaunchCompletion();  // the join grid may take its place; it waits for this one to end
     const uint32_t tmem = ms.tmem;
     bool ok = true;
-    auto live_rows = [&]() -> int32_t { return min(p.npt, w.req.n - node0) * p.Gc; };  // <= 0: nothing for this CTA
+    // (the odd CTA of a pair may have no row of its own, but shares the work on the even one's)
+    auto skip = [&]() -> bool { return w.req.n <= lead0; };
+    // a tile with V rows that no node sees
+    auto edge_of = [&](int32_t tile) -> bool {
+        const int32_t key0 = (w.req.tile0 + w.t0 + tile) * kTile;
+        return key0 < w.req.lo || key0 + kTile > w.req.L;
+    };
+    // zeroes those rows of a V stage (its keys begin at key0); 0 x NaN would reach every row
+    auto clean = [&](uint8_t* stg, int32_t key0) {
+        for (int idx = lane; idx < kStageBytes / 16; idx += 32) {
+            const int32_t key = key0 + (idx / 8) % kVKeys;
+            if (key < w.req.lo || key >= w.req.L) *reinterpret_cast<uint4*>(stg + idx * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
 
     if (warp >= kProducerWarp && warp < kProducerWarp + kProducers) {
         // ------------------------------------------------------------------ TMA producers
         const int pw = warp - kProducerWarp;
         const uint64_t kv_policy = l2_policy_evict_first();
-        const int32_t boxes = kTile / x.box;                 // per stage, K and V alike
+        const int32_t boxes = kTile / x.box;  // per stage, K and V alike
+        const bool once = p.n_sub == (kPair ? 2 : 1);
         RingPos pos{pw, 0u};
         uint32_t issued = 0, issued_phase = 0, q_phase = 0;
         bool q_out = false;
         int32_t skew = pw;  // this warp's next stage of the piece: every third one, counted across pieces
         for (; !w.done() && ok; w.next(p)) {
-            const int32_t live = live_rows();
-            if (live <= 0) continue;
-            const bool two = kAlternate && live > 128;
+            if (skip()) continue;
             const int32_t n = w.t1 - w.t0;
-            const int32_t total = n * (kc_n + vs_n);
+            const int32_t total = n * (ks_n + vs_n);
             if (pw == 0) {
                 // Q once the last piece's scores are computed
+                ok = __all_sync(0xffffffffu, bounded_wait(&ms.q_free, q_phase ^ 1u));
+                if (!ok) break;
                 if (lane == 0) {
-                    ok = ring_wait(&ms.q_free, q_phase ^ 1u, abort_flag, p.err, p.wait_ns);
-                    if (ok) {
-                        mbar_expect_tx(&ms.q_full, (uint32_t)(kc_n * p.rows * 128));
-                        for (int kc = 0; kc < kc_n; ++kc)
-                            tma_load_3d(q_s + (size_t)kc * x.q_rows * 128, &tm_q, &ms.q_full, kc * 64,
-                                        w.g * p.G + st.gc * p.Gc, w.b * p.T + node0);
+                    const uint32_t bytes = (uint32_t)(kc_n * p.rows * 128);
+                    if (leader) mbar_expect_tx(&ms.q_full, kPair ? 2 * bytes : bytes);
+                    for (int kc = 0; kc < kc_n; ++kc) {
+                        uint8_t* dst = q_s + (size_t)kc * x.q_rows * 128;
+                        const int32_t head = w.g * p.G + st.gc * p.Gc;
+                        if (kPair)
+                            tma_load_3d_pair(dst, &tm_q, lead_bar(&ms.q_full), kc * 64, head, w.b * p.T + node0);
+                        else
+                            tma_load_3d(dst, &tm_q, &ms.q_full, kc * 64, head, w.b * p.T + node0);
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
+                __syncwarp();
                 q_phase ^= 1u;
                 q_out = true;
             }
@@ -298,22 +358,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto box_of = [&](int32_t i) -> Box {
                 Box bx{p.num_pages, 0, 0, 0};
                 if (lane >= boxes) return bx;
-                const StageOf so = stage_of(i, n, two, kc_n, vs_n);
+                const StageOf so = stage_of(i, n, ks_n, vs_n);
                 int32_t key = (w.req.tile0 + w.t0 + so.tile) * kTile;
+                const int32_t per = boxes / 2, slab = lane / per, i2 = lane - slab * per;  // of two 64-dim slabs
+                bool slabs;
                 if (so.is_k) {
-                    key += lane * x.box;
-                    bx.dim = so.sub * 64;
-                    bx.dst = lane * x.box * 128;
-                } else if (DV == 64) {
-                    key += lane * x.box;
-                    bx.dim = 0;
-                    bx.dst = lane * x.box * 128;
+                    slabs = kPair;
+                    key += kPair ? (int32_t)rank * 64 : 0;
+                    bx.dim = so.sub * (kPair ? 128 : 64);
                 } else {
-                    const int32_t per = boxes / 2, h = so.sub / vc_n, c = so.sub - h * vc_n;
-                    const int32_t slab = lane / per, i2 = lane - slab * per;
-                    key += h * 64 + i2 * x.box;
-                    bx.dim = st.dv * DV + c * 128 + slab * 64;
+                    slabs = kVKeys == 64;
+                    const int32_t h = so.sub / vc_n, c = so.sub - h * vc_n;
+                    key += h * kVKeys;
+                    bx.dim = st.dv * DV + c * kVN + (int32_t)rank * (kVN / 2);
+                }
+                if (slabs) {
+                    key += i2 * x.box;
+                    bx.dim += slab * 64;
                     bx.dst = slab * 8192 + i2 * x.box * 128;
+                } else {
+                    key += lane * x.box;
+                    bx.dst = lane * x.box * 128;
                 }
                 if (key < w.req.L && key + x.box > w.req.lo) {
                     const int32_t pg = key / p.page_size;
@@ -333,20 +398,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; i < total; i += kProducers) {
                 Box nxt{p.num_pages, 0, 0, 0};
                 if (i + kProducers < total) nxt = box_of(i + kProducers);
-                if (lane == 0) {
-                    ok = ring_wait(ms.empty + pos.idx, pos.phase ^ 1u, abort_flag, p.err, p.wait_ns);
-                    if (ok) mbar_expect_tx(ms.full + pos.idx, kStageBytes);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                ok = __all_sync(0xffffffffu, bounded_wait(ms.empty + pos.idx, pos.phase ^ 1u));
                 if (!ok) break;
+                const StageOf so = stage_of(i, n, ks_n, vs_n);
+                // Pair: the even CTA's barrier counts both halves of a stage; but where V rows have to be zeroed
+                // each CTA's counts its own, and the odd one reports when it has done so (v_clean).
+                const bool apart = kPair && !so.is_k && edge_of(so.tile);
+                if (lane == 0 && (leader || apart))
+                    mbar_expect_tx(ms.full + pos.idx, kPair && !apart ? 2 * kStageBytes : kStageBytes);
+                __syncwarp();
                 if (lane < boxes) {
-                    const CUtensorMap* map = stage_of(i, n, two, kc_n, vs_n).is_k ? &tm_k : &tm_v;
+                    const CUtensorMap* map = so.is_k ? &tm_k : &tm_v;
                     uint8_t* dst = ring + (size_t)pos.idx * kStageBytes + cur.dst;
                     // read once: the first to leave L2, unless other query tiles read it again
-                    if (p.n_sub == 1)
+                    if (kPair) {
+                        const uint32_t bar = mapa_shared(smem_u32(ms.full + pos.idx), apart ? rank : 0u);
+                        if (once)
+                            tma_load_4d_pair_hint(dst, map, bar, cur.dim, w.g, cur.slot, cur.page, kv_policy);
+                        else
+                            tma_load_4d_pair(dst, map, bar, cur.dim, w.g, cur.slot, cur.page);
+                    } else if (once) {
                         tma_load_4d_hint(dst, map, ms.full + pos.idx, cur.dim, w.g, cur.slot, cur.page, kv_policy);
-                    else
+                    } else {
                         tma_load_4d(dst, map, ms.full + pos.idx, cur.dim, w.g, cur.slot, cur.page);
+                    }
                 }
                 __syncwarp();
                 issued |= 1u << pos.idx;
@@ -356,22 +431,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             skew = i - total;
         }
-        // no copy of ours may land after the CTA has gone
+        // No copy of ours may land after the CTA has gone. The odd CTA's are counted at the even one's barriers, which
+        // it cannot wait on: it gives them time.
         if (!ok && lane == 0) {
             const unsigned long long t0 = globaltimer();
-            for (int s = 0; s < S; ++s)
-                if (issued & (1u << s))
-                    while (!mbar_test_wait(ms.full + s, (issued_phase >> s) & 1u) && globaltimer() - t0 < p.wait_ns) {
+            if (leader) {
+                for (int s = 0; s < S; ++s)
+                    if (issued & (1u << s))
+                        while (!mbar_test_wait(ms.full + s, (issued_phase >> s) & 1u) && globaltimer() - t0 < p.wait_ns) {
+                        }
+                if (q_out)
+                    while (!mbar_test_wait(&ms.q_full, q_phase ^ 1u) && globaltimer() - t0 < p.wait_ns) {
                     }
-            if (q_out)
-                while (!mbar_test_wait(&ms.q_full, q_phase ^ 1u) && globaltimer() - t0 < p.wait_ns) {
+            }
+            if (kPair)
+                while (globaltimer() - t0 < kCopyGraceNs) {
                 }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp && leader) {
         // ------------------------------------------------------------------ MMA issuer
-        constexpr uint32_t idesc_s = make_idesc(128, kTile, 0, 0);
-        constexpr uint32_t idesc_o = make_idesc(128, kVN, 0, 1);
+        constexpr uint32_t idesc_s = make_idesc(kM, kTile, 0, 0);
+        constexpr uint32_t idesc_o = make_idesc(kM, kVN, 0, 1);
         // Descriptors are made once: a later operand is its base plus an offset in 16-byte units. Everything about an
         // MMA but the issue itself is the same for the whole warp, so that it lies in uniform registers, where the
         // instruction wants it; with the operands worked out by one thread an MMA took about 150 cycles to issue.
@@ -379,178 +460,202 @@ __global__ void __launch_bounds__(kThreads, 1)
                        v_desc = sw128_desc(smem_u32(ring), 8192, 1024);
         const uint32_t q_chunk = (uint32_t)x.q_rows * 8;  // one 64-dim chunk of Q
         RingPos pos{0, 0u};
-        uint32_t q_phase = 0, p_phase = 0;  // p_phase: bit b = parity of the next P in buffer b
+        // p_phase: bit b = parity of the next P in buffer b; clean_phase: bit s = of slot s's next zeroed V stage
+        uint32_t q_phase = 0, p_phase = 0, clean_phase = 0;
         auto wait0 = [&](uint64_t* bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, ring_wait(bar, parity, abort_flag, p.err, p.wait_ns));
+            return __all_sync(0xffffffffu, bounded_wait(bar, parity));
         };
         for (; !w.done() && ok; w.next(p)) {
-            const int32_t live = live_rows();
-            if (live <= 0) continue;
-            const bool two = kAlternate && live > 128;
-            const int32_t n = w.t1 - w.t0, steps = two ? 2 * n : n;
+            if (skip()) continue;
+            const int32_t steps = w.t1 - w.t0;
             ok = wait0(&ms.q_full, q_phase);
             if (!ok) break;
             q_phase ^= 1u;
-            // S(t) = Q K^T. `fresh`: the first use of the tile's stages (they are waited for); `last`: the
-            // last (they are released). Otherwise the stages stay for the other row tile, and `at` is where they begin.
-            auto scores = [&](int32_t t, RingPos at, bool fresh, bool last) {
+            // S(t) = Q K^T
+            auto scores = [&](int32_t t) {
                 const uint32_t d = tmem + (uint32_t)(t & 1) * 128;
-                uint64_t qd = q_desc + (two ? (uint32_t)(t & 1) * 1024 : 0u);
+                uint64_t qd = q_desc;
 #pragma unroll 1
-                for (int kc = 0; kc < kc_n && ok; ++kc) {
-                    if (fresh) ok = wait0(ms.full + at.idx, at.phase);
-                    if (!ok) break;
-                    const uint64_t kd = k_desc + (uint32_t)at.idx * (kStageBytes / 16);
+                for (int ks = 0; ks < ks_n; ++ks) {
+                    ok = wait0(ms.full + pos.idx, pos.phase);
+                    if (!ok) return;
+                    const uint64_t kd = k_desc + (uint32_t)pos.idx * (kStageBytes / 16);
+                    const bool second = kPair && 2 * ks + 1 < kc_n;  // the stage's second slab holds dims
                     if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma(d, qd + 2 * kk, kd + 2 * kk, idesc_s, (kc > 0 || kk > 0) ? 1u : 0u);
-                        if (last) tc_commit(ms.empty + at.idx);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (kPair)
+                                tc_mma2(d, qd + 2 * kk, kd + 2 * kk, idesc_s, (ks > 0 || kk > 0) ? 1u : 0u);
+                            else
+                                tc_mma(d, qd + 2 * kk, kd + 2 * kk, idesc_s, (ks > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        if (second) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma2(d, qd + q_chunk + 2 * kk, kd + 512 + 2 * kk, idesc_s, 1u);
+                        }
+                        commit(ms.empty + pos.idx);
                     }
                     __syncwarp();
-                    qd += q_chunk;
-                    at.advance(1, S);
+                    qd += kPair ? 2 * q_chunk : q_chunk;
+                    pos.advance(1, S);
                 }
-                if (ok && elect_one()) {
-                    tc_commit(ms.s_full + (t & 1));
-                }
+                if (elect_one()) commit(ms.s_full + (t & 1));
                 __syncwarp();
-                return at;
             };
             // O += P(t) V
-            auto values = [&](int32_t t, RingPos at, bool fresh, bool last) {
-                const int32_t tile = two ? t >> 1 : t;
+            auto values = [&](int32_t t) {
                 const int32_t slot = kAlternate ? t & 1 : 0;
                 const bool first = kAlternate ? t < 2 : t == 0;
                 const uint32_t d = tmem + kOCol + (uint32_t)slot * 128;
                 const uint32_t pa = tmem + (uint32_t)(t & 1) * 128;
-                const int32_t key0 = (w.req.tile0 + w.t0 + tile) * kTile;
+                const bool edge = edge_of(t);
                 // the first 64 keys' probabilities come ahead of the rest
                 ok = wait0(ms.p_half + (t & 1), (p_phase >> (t & 1)) & 1u);
+                if (!ok) return;
                 tc_fence_after();
-                if (DV == 64 && ok) {  // a V stage is 128 keys
-                    ok = wait0(ms.p_full + (t & 1), (p_phase >> (t & 1)) & 1u);
-                    tc_fence_after();
-                }
-                const bool edge = key0 < w.req.lo || key0 + kTile > w.req.L;
 #pragma unroll 1
-                for (int sv = 0; sv < vs_n && ok; ++sv) {
+                for (int sv = 0; sv < vs_n; ++sv) {
                     const int32_t h = sv / vc_n, c = sv - h * vc_n;
-                    if (DV != 64 && sv == vc_n) {
+                    if (h == 1 && c == 0) {
                         ok = wait0(ms.p_full + (t & 1), (p_phase >> (t & 1)) & 1u);
+                        if (!ok) return;
                         tc_fence_after();
-                        if (!ok) break;
                     }
-                    if (fresh) {
-                        ok = wait0(ms.full + at.idx, at.phase);
-                        if (!ok) break;
-                        if (edge) {
-                            // rows of keys that no node sees
-                            uint8_t* stg = ring + (size_t)at.idx * kStageBytes;
-                            for (int idx = lane; idx < kStageBytes / 16; idx += 32) {
-                                const int32_t key = key0 + h * kVKeys + (idx / 8) % kVKeys;
-                                if (key < w.req.lo || key >= w.req.L)
-                                    *reinterpret_cast<uint4*>(stg + idx * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
+                    ok = wait0(ms.full + pos.idx, pos.phase);
+                    if (!ok) return;
+                    if (edge) {
+                        clean(ring + (size_t)pos.idx * kStageBytes, (w.req.tile0 + w.t0 + t) * kTile + h * kVKeys);
+                        if (kPair) {
+                            // (the odd CTA's ordinary stores come before its arrival)
+                            ok = __all_sync(0xffffffffu,
+                                            ring_wait_cluster(ms.v_clean + pos.idx, (clean_phase >> pos.idx) & 1u,
+                                                              abort_flag, p.err, p.wait_ns));
+                            if (!ok) return;
+                            clean_phase ^= 1u << pos.idx;
                         }
                     }
-                    const uint64_t vd = v_desc + (uint32_t)at.idx * (kStageBytes / 16);
+                    const uint64_t vd = v_desc + (uint32_t)pos.idx * (kStageBytes / 16);
                     const uint32_t dc = d + (uint32_t)c * 128, ph = pa + (uint32_t)(h * kVKeys) / 2;
-                    if (elect_one()) {
+                    auto part = [&](int k0) {
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < kVKeys / 16; ++kk)
-                            tc_mma_ta(dc, ph + kk * 8, vd + kk * 128, idesc_o, (!first || h > 0 || kk > 0) ? 1u : 0u);
-                        if (last) tc_commit(ms.empty + at.idx);
+                            for (int kk = k0; kk < k0 + 4; ++kk) {
+                                const uint32_t more = (!first || h > 0 || kk > 0) ? 1u : 0u;
+                                if (kPair)
+                                    tc_mma2_ta(dc, ph + kk * 8, vd + kk * 128, idesc_o, more);
+                                else
+                                    tc_mma_ta(dc, ph + kk * 8, vd + kk * 128, idesc_o, more);
+                            }
+                        }
+                        __syncwarp();
+                    };
+                    part(0);
+                    if (kVKeys == 128) {
+                        ok = wait0(ms.p_full + (t & 1), (p_phase >> (t & 1)) & 1u);
+                        if (!ok) return;
+                        tc_fence_after();
+                        part(4);
                     }
+                    if (elect_one()) commit(ms.empty + pos.idx);
                     __syncwarp();
-                    at.advance(1, S);
+                    pos.advance(1, S);
                 }
                 p_phase ^= 1u << (t & 1);
-                if (ok && elect_one()) tc_commit(ms.o_done + slot);
+                if (elect_one()) commit(ms.o_done + slot);
                 __syncwarp();
-                return at;
             };
-            if (two) {
-                RingPos v_at{0, 0u}, k_at = pos;
-                pos = scores(0, k_at, true, false);
-                if (ok) scores(1, k_at, false, true);
+            scores(0);
+            if (ok && steps > 1) scores(1);
 #pragma unroll 1
-                for (int32_t j = 0; j < n && ok; ++j) {
-                    v_at = pos;
-                    pos = values(2 * j, v_at, true, false);
-                    k_at = pos;
-                    if (ok && j + 1 < n) pos = scores(2 * j + 2, k_at, true, false);
-                    if (ok) values(2 * j + 1, v_at, false, true);
-                    if (ok && j + 1 < n) scores(2 * j + 3, k_at, false, true);
-                }
-            } else {
-                pos = scores(0, pos, true, true);
-                if (ok && steps > 1) pos = scores(1, pos, true, true);
-#pragma unroll 1
-                for (int32_t t = 0; t < steps && ok; ++t) {
-                    pos = values(t, pos, true, true);
-                    if (ok && t + 2 < steps) pos = scores(t + 2, pos, true, true);
-                }
+            for (int32_t t = 0; t < steps && ok; ++t) {
+                values(t);
+                if (ok && t + 2 < steps) scores(t + 2);
             }
-            if (ok && elect_one()) tc_commit(&ms.q_free);
+            if (ok && elect_one()) commit(&ms.q_free);
             __syncwarp();
         }
         // our MMAs end before TMEM is freed
         if (elect_one()) {
-            tc_commit(&ms.drain);
+            if (kPair)
+                tc_commit2_local(&ms.drain);
+            else
+                tc_commit(&ms.drain);
             const unsigned long long t0 = globaltimer();
             while (!mbar_test_wait(&ms.drain, 0) && globaltimer() - t0 < p.wait_ns) {
             }
         }
         __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------------ odd CTA: rows of V to zero
+        RingPos pos{0, 0u};
+        uint32_t seen = 0;  // bit s: parity of the next stage counted at this CTA's own full[s]
+        for (; !w.done() && ok; w.next(p)) {
+            if (skip()) continue;
+            const int32_t n = w.t1 - w.t0;
+            const int32_t total = n * (ks_n + vs_n);
+#pragma unroll 1
+            for (int32_t i = 0; i < total && ok; ++i, pos.advance(1, S)) {
+                const StageOf so = stage_of(i, n, ks_n, vs_n);
+                if (so.is_k || !edge_of(so.tile)) continue;
+                ok = __all_sync(0xffffffffu, bounded_wait(ms.full + pos.idx, (seen >> pos.idx) & 1u));
+                if (!ok) break;
+                seen ^= 1u << pos.idx;
+                clean(ring + (size_t)pos.idx * kStageBytes, (w.req.tile0 + w.t0 + so.tile) * kTile + so.sub * kVKeys);
+                if (lane == 0) mbar_arrive_cluster(lead_bar(ms.v_clean + pos.idx));
+                __syncwarp();
+            }
+        }
     } else {
         // ------------------------------------------------------------------ softmax and output
         const int wg = warp >> 2;
-        const int r128 = tid & 127;
+        const int row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl2 = p.scale * kLog2e;
         const int words = (p.T + 31) / 32;
         uint32_t s_phase = 0, o_phase = 0;  // bit b: parity of the next phase of buffer / slot b
         auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-            if (ok) {
-                bool got = true;
-                if (lane == 0) got = ring_wait(bar, parity, abort_flag, p.err, p.wait_ns);
-                ok = __shfl_sync(0xffffffffu, got, 0);
-            }
+            if (ok) ok = __all_sync(0xffffffffu, bounded_wait(bar, parity));
             tc_fence_after();
+        };
+        // a softmax warp's part of P is in TMEM
+        auto arrive = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair && !leader)
+                    arrive_peer(lead_bar(bar));
+                else
+                    mbar_arrive(bar);
+            }
         };
         // A failed wait ends the computation, not the walk: the barriers below are met by every thread.
         for (; !w.done(); w.next(p)) {
-            const int32_t live = live_rows();
-            if (live <= 0) continue;
-            const bool two = kAlternate && live > 128;
-            const int32_t n = w.t1 - w.t0, steps = two ? 2 * n : n;
+            if (skip()) continue;
+            const int32_t live = min(p.npt, w.req.n - node0) * p.Gc;  // rows of this CTA with a node; <= 0: none
+            const int32_t steps = w.t1 - w.t0;
             const int32_t ctx = w.req.ctx;
             const int32_t first_key = (w.req.tile0 + w.t0) * kTile, end_key = (w.req.tile0 + w.t1) * kTile;
             const int32_t win_end = p.window > 0 ? ctx + w.req.n - p.window : 0;  // keys from here on: no window's edge
             if (end_key > ctx || first_key < win_end) {
-                named_bar_sync_256();  // the last piece's masks are done with
+                // (the barrier that ended the last piece keeps its masks from being overwritten)
                 tree_load_parents(p, w.b, w.req.n, ms.par, tid, 256);
                 named_bar_sync_256();
                 tree_walk_nodes(p, w.req, node0, min(p.npt, w.req.n - node0), ms.par, anc_s, lo_s, tid, 256);
                 named_bar_sync_256();
             }
-            const int32_t row = (two ? wg * 128 : 0) + r128;
             const bool live_row = row < live;
             const int32_t nd = row / p.Gc;
             const uint32_t* anc = anc_s + nd * words;
             const int32_t slot = kAlternate ? wg : 0;
             const uint32_t o_addr = tmem + kOCol + (uint32_t)slot * 128 + lanes;
-            const int32_t t_step = kAlternate ? 2 : 1;
             const int32_t d_here = min(DV, p.D - st.dv * DV);
             float m2 = -INFINITY, l = 0.f;
             bool any = false;  // this slot has had a step in the piece
 #pragma unroll 1
-            for (int32_t t = kAlternate ? wg : 0; t < steps && (kAlternate || wg == 0); t += t_step) {
+            for (int32_t t = kAlternate ? wg : 0; t < steps && (kAlternate || wg == 0); t += kAlternate ? 2 : 1) {
                 const int buf = t & 1;
-                const int32_t key0 = first_key + (two ? t >> 1 : t) * kTile;
+                const int32_t key0 = first_key + t * kTile;
                 const bool edge = key0 + kTile > ctx || key0 < win_end;
                 const uint32_t s_addr = tmem + (uint32_t)buf * 128 + lanes;
                 wait_warp(ms.s_full + buf, (s_phase >> buf) & 1u);
@@ -616,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     waited = true;
                     if (ok) {
 #pragma unroll 1
-                        for (int c = 0; c < d_here; c += 32) {
+                        for (int c = 0; c < d_here; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(o_addr + c, o);
                             tmem_ld_wait();
@@ -656,8 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // every phase of o_done is waited for once, so that its parity tells them apart
                     if (h == 0 && any && !waited) wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
-                    tc_fence_before();
-                    mbar_arrive((h == 0 ? ms.p_half : ms.p_full) + buf);
+                    arrive((h == 0 ? ms.p_half : ms.p_full) + buf);
                 }
                 if (any) o_phase ^= 1u << slot;
                 any = true;
@@ -674,49 +778,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t prow = tree_part_row(p, range, sub, w.slot()) + row;
             const int32_t node = node0 + nd, head = w.g * p.G + st.gc * p.Gc + (row - nd * p.Gc);
             const int64_t orow = ((int64_t)w.b * p.T + node) * p.Hq + head;
-            float f0, f1 = 0.f, lse2;
-            if (two) {
-                f0 = l > 0.f ? 1.f / l : 0.f;
-                lse2 = l > 0.f ? m2 + __log2f(l) : -INFINITY;
-            } else {
-                tc_fence_before();
-                ms.m[wg][r128] = m2;
-                ms.l[wg][r128] = l;
-                named_bar_sync_256();
-                tc_fence_after();
-                const float ma = ms.m[0][r128], mb = ms.m[1][r128];
-                const float mm = fmaxf(ma, mb);
-                const float wa = ma == -INFINITY ? 0.f : ex2(ma - mm), wb = mb == -INFINITY ? 0.f : ex2(mb - mm);
-                const float tot = ms.l[0][r128] * wa + ms.l[1][r128] * wb;
-                const float inv = tot > 0.f ? 1.f / tot : 0.f;
-                f0 = wa * inv;
-                f1 = wb * inv;
-                lse2 = tot > 0.f ? mm + __log2f(tot) : -INFINITY;
-            }
-            if (live_row && st.dv == 0 && (two || wg == 0)) {
-                const float lse = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
+            // the row's two accumulators (or one, beside nothing) about their common maximum
+            tc_fence_before();
+            ms.m[wg][row] = m2;
+            ms.l[wg][row] = l;
+            named_bar_sync_256();
+            tc_fence_after();
+            const float ma = ms.m[0][row], mb = ms.m[1][row];
+            const float mm = fmaxf(ma, mb);
+            const float wa = ma == -INFINITY ? 0.f : ex2(ma - mm), wb = mb == -INFINITY ? 0.f : ex2(mb - mm);
+            const float tot = ms.l[0][row] * wa + ms.l[1][row] * wb;
+            const float inv = tot > 0.f ? 1.f / tot : 0.f;
+            const float f0 = wa * inv, f1 = wb * inv;
+            if (live_row && wg == 0) {
+                const float lse = tot > 0.f ? (mm + __log2f(tot)) * kLn2 : -INFINITY;
                 if (!whole)
                     p.part_lse[prow] = lse;
-                else if (p.lse)
+                else if (p.lse && st.dv == 0)
                     p.lse[orow] = lse;
             }
-            if (live_row && st.dv != 0 && wg == 0 && !whole) p.part_lse[prow] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
-            // two row tiles: a warpgroup writes its own rows; one: each half of the columns
-            const int32_t c_begin = two ? 0 : wg * (DV / 2), c_end = min(d_here, two ? DV : c_begin + DV / 2);
-            const uint32_t own = tmem + kOCol + (two ? (uint32_t)slot * 128 : 0u) + lanes;
-            const bool second = kAlternate && !two && steps > 1;
+            // each warpgroup writes half of the columns
+            const int32_t c_begin = wg * (DV / 2), c_end = min(d_here, c_begin + DV / 2);
+            const uint32_t o0 = tmem + kOCol + lanes;
+            const bool second = kAlternate && steps > 1;
             if (ok) {
 #pragma unroll 1
                 for (int32_t c = c_begin; c < c_end; c += 16) {
                     uint32_t r[16];
-                    tmem_ld16(own + c, r);
+                    tmem_ld16(o0 + c, r);
                     tmem_ld_wait();
                     reg_fence16(r);
                     float o[16];
 #pragma unroll
                     for (int u = 0; u < 16; ++u) o[u] = u2f(r[u]) * f0;
                     if (second) {
-                        tmem_ld16(own + 128 + c, r);
+                        tmem_ld16(o0 + 128 + c, r);
                         tmem_ld_wait();
                         reg_fence16(r);
 #pragma unroll
@@ -742,15 +838,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc_fence_before();
-            if (!two) named_bar_sync_256();  // O and the sums are read before the next piece's steps
+            named_bar_sync_256();  // O, the sums and the masks are read before the next piece's steps
         }
     }
     // ---------------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync_all();  // no CTA leaves while the pair's MMAs or the peer may touch its memory
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if (kPair)
+            tmem_dealloc2(tmem, 512);
+        else
+            tmem_dealloc(tmem, 512);
     }
 }
 
@@ -784,24 +884,67 @@ bool encode(EncodeTiledFn enc, CUtensorMap* map, const void* base, int rank, con
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+std::mutex g_pairs_mutex;
+int g_pairs[64][2] = {};  // resident CTA pairs per device, of DV = 128 and 256
+
+// CTA pairs that are resident at once: a pair more would run after all the others.
 template <int DV>
-cudaError_t launch_dv(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeAttnParams& p,
+int resident_pairs()
+{
+    int dev = 0;
+    const int guess = device_sm_count() / 2;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return guess;
+    std::lock_guard<std::mutex> lk(g_pairs_mutex);
+    int& n = g_pairs[dev][DV == 256];
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemMax;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int found = 0;
+        if (cudaOccupancyMaxActiveClusters(&found, tree_attn_tc_kernel<DV, true>, &cfg) != cudaSuccess || found < 1) {
+            (void)cudaGetLastError();
+            return guess;
+        }
+        n = found;
+    }
+    return n;
+}
+
+template <int DV, bool kPair>
+cudaError_t launch_dv(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeAttnParams& p, int32_t box,
                       cudaStream_t stream)
 {
     TcShape x;
     x.q_rows = (p.rows + 7) / 8 * 8;
-    x.box = 8;
-    while (x.box < 64 && p.page_size % (2 * x.box) == 0) x.box *= 2;
+    x.box = box;
     const int32_t q_bytes = (p.D + 63) / 64 * x.q_rows * 128;
     const int32_t misc = (int32_t)sizeof(TcMisc) + p.npt * 4 * (1 + (p.T + 31) / 32);
     x.stages = std::min(kMaxStages, (kSmemMax - 1024 - q_bytes - misc) / kStageBytes);
-    // Q's 128- or 256-row reads past its last row end inside the ring
+    // Q's 128-row reads past its last row end inside the ring
     if (x.stages < 4) return cudaErrorInvalidConfiguration;
-    const int32_t bytes = 1024 + q_bytes + x.stages * kStageBytes + misc;
-    cudaError_t e = cudaFuncSetAttribute(tree_attn_tc_kernel<DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e =
+        cudaFuncSetAttribute(tree_attn_tc_kernel<DV, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
-    tree_attn_tc_kernel<DV><<<p.ranges * p.n_sub, kThreads, bytes, stream>>>(tq, tk, tv, p, x);
-    return cudaGetLastError();
+    if constexpr (kPair) p.ranges = std::max(1, std::min(p.ranges, 2 * resident_pairs<DV>() / p.n_sub));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.ranges * p.n_sub));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 1024 + q_bytes + x.stages * kStageBytes + misc;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, tree_attn_tc_kernel<DV, kPair>, tq, tk, tv, static_cast<const TreeAttnParams&>(p), x);
 }
 
 }  // namespace
@@ -816,7 +959,7 @@ bool tree_tc_supports(const dflash_dims* d)
     return d->kv_stride_slot < most && d->kv_stride_head < most && d->kv_stride_page < most;
 }
 
-cudaError_t launch_tree_attn_tc(const TreeAttnParams& p, cudaStream_t stream)
+cudaError_t launch_tree_attn_tc(TreeAttnParams& p, cudaStream_t stream)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
@@ -834,10 +977,13 @@ cudaError_t launch_tree_attn_tc(const TreeAttnParams& p, cudaStream_t stream)
     if (!encode(enc, &tq, p.q, 3, qd, qs, qb) || !encode(enc, &tk, p.k, 4, kd, ks, kb) ||
         !encode(enc, &tv, p.v, 4, kd, ks, kb))
         return cudaErrorInvalidValue;
+    if (p.pair)
+        return p.DV == 128 ? launch_dv<128, true>(tq, tk, tv, p, box, stream)
+                           : launch_dv<256, true>(tq, tk, tv, p, box, stream);
     switch (p.DV) {
-    case 64: return launch_dv<64>(tq, tk, tv, p, stream);
-    case 128: return launch_dv<128>(tq, tk, tv, p, stream);
-    default: return launch_dv<256>(tq, tk, tv, p, stream);
+    case 64: return launch_dv<64, false>(tq, tk, tv, p, box, stream);
+    case 128: return launch_dv<128, false>(tq, tk, tv, p, box, stream);
+    default: return launch_dv<256, false>(tq, tk, tv, p, box, stream);
     }
 }
 

@@ -4,19 +4,17 @@
 //   S [128 rows x 128 keys] = Q [128 x D] . K^T        (A: Q in shared memory, B: the K tile)
 //   O [128 rows x DV]      += P [128 x 128] . V        (A: P in TMEM, B: the V tile, MN-major)
 //
-// A query row is a (node, head of the KV head's group); a softmax thread owns a TMEM lane, that is a whole row, so the
-// row maximum and sum need no exchange between threads. P (bf16) overwrites its own S, thus costs
+// A query row is a (node, head of the KV head's group), a TMEM lane. Two softmax threads share a row's tile, 64 keys each:
+// they read their scores once into registers, exchange one maximum through shared memory, and hand over their half
+// of P. (A thread per row, alternate tiles to two warpgroups and O accumulators, took 1.45 us a
+// tile, two passes over TMEM, on the way between two MMAs: 158 us for the ragged batch of 64-node trees.) P (bf16) overwrites its own S, thus costs
 // neither shared memory nor TMEM, and shared memory is left to Q and the ring: what bounds the kernel is
 // the K/V stream, whose rate is the bytes in flight over the latency.
 //
-// TMEM (512 columns): S0, S1 (128 each) and 256 columns of O. A query tile is up to 128 rows; step t of a piece (one
-// range's part of a request and KV head) is its key tile t, with S buffer t % 2:
-//   DV <= 128: two O accumulators, of even and odd steps: two warpgroups take alternate tiles with a maximum, a sum and an
-//     O each, joined when the piece ends, so neither waits for the other;
-//   DV = 256: one O, one warpgroup; S(t+1) is computed while the softmax of S(t) runs. For head_dim above 256 a CTA
-//     computes 256 of the output's dims from the whole S.
-// The MMA warp does: S(0), S(1), then for every t: O += P(t) V, S(t + 2), which reuses the buffer of P(t) (MMAs of one
-// thread execute in order).
+// TMEM (512 columns): S0, S1 (128 each) and up to 256 of O; for head_dim above 256 a CTA computes 256 of the output's dims from
+// the whole S. A query tile is up to 128 rows; step t of a piece (one range's part of a request and KV head) is its key
+// tile t, with S buffer t % 2. The MMA warp does: S(0), S(1), then for every t: O += P(t) V, S(t + 2), which reuses the
+// buffer of P(t) (MMAs of one thread execute in order), so S(t + 1) waits for the softmax while S(t)'s P is multiplied.
 //
 // More than 128 rows per KV head: CTA pairs (clusters of two, cta_group::2). The two CTAs hold neighbouring query tiles and
 // share every MMA (M = 256): each loads half of the K tile's keys and half of the V tile's dims, so a K/V byte
@@ -35,7 +33,7 @@
 // one word, made from its ancestors' bits. V rows that no node sees are zeroed in shared memory, as 0 x NaN would
 // reach every row.
 //
-// Warps: 0-3 and 4-7 softmax and output, 8-10 TMA producers, 11 the MMA issuer. Ring stages are 16 KB: K 128 keys
+// Warps: 0-7 softmax and output, 8-10 TMA producers, 11 the MMA issuer. Ring stages are 16 KB: K 128 keys
 // x 64 dims, V 64 keys x 128 dims (128 keys x 64 dims at DV = 64); in a pair each CTA's halves are K 64 keys x
 // 128 dims, V 64 keys x 128 dims (DV = 256) or 128 keys x 64 dims. A box is 64 dims of up to 64 tokens of one page; its
 // id is read one stage ahead by the lane that issues it. Boxes past the keys or before the window are
@@ -57,6 +55,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 384;
+constexpr int kSoftmax = 256;  // warps 0-7
 constexpr int kProducerWarp = 8;
 constexpr int kProducers = 3;
 constexpr int kMmaWarp = 11;
@@ -80,12 +79,13 @@ struct TcShape {
 struct TcMisc {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_free;
-    uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_done;
     uint64_t v_clean[kMaxStages];  // pair: the odd CTA has zeroed its rows of the slot's V stage
     uint64_t drain;
     uint32_t tmem;
     int32_t abort;
-    float m[2][128], l[2][128];
+    float mx[2][2][128];  // row maxima of tile t over half of its keys, in [t % 2]
+    float l[2][128];
     int32_t par[DFLASH_MAX_TREE_NODES];
     // then lo [npt], ancestor words [npt][(T + 31) / 32]
 };
@@ -223,7 +223,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_v, const TreeAttnParams p, const TcShape x)
 {
     static_assert(DV == 256 || DV == 128 || (DV == 64 && !kPair), "64 dims in halves of 32 have no 128-byte rows");
-    constexpr bool kAlternate = DV <= 128;                            // two O accumulators
     constexpr int kVN = kPair ? DV : DV == 64 ? 64 : 128;             // dims of a V stage (both CTAs' of a pair)
     constexpr int kVKeys = kPair ? (DV == 256 ? 64 : 128) : DV == 64 ? 128 : 64;  // and its keys
     constexpr int kM = kPair ? 256 : 128;
@@ -274,10 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ms.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(ms.s_full + i, 1);
-            mbar_init(ms.p_half + i, kPair ? 8 : 4);  // a softmax warp each
+            mbar_init(ms.p_half + i, kPair ? 16 : 8);  // a softmax warp each
             mbar_init(ms.p_full + i, kPair ? 8 : 4);
-            mbar_init(ms.o_done + i, 1);
         }
+        mbar_init(&ms.o_done, 1);
         mbar_init(&ms.drain, 1);
         ms.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -505,9 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // O += P(t) V
             auto values = [&](int32_t t) {
-                const int32_t slot = kAlternate ? t & 1 : 0;
-                const bool first = kAlternate ? t < 2 : t == 0;
-                const uint32_t d = tmem + kOCol + (uint32_t)slot * 128;
+                const bool first = t == 0;
+                const uint32_t d = tmem + kOCol;
                 const uint32_t pa = tmem + (uint32_t)(t & 1) * 128;
                 const bool edge = edge_of(t);
                 // the first 64 keys' probabilities come ahead of the rest
@@ -562,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pos.advance(1, S);
                 }
                 p_phase ^= 1u << (t & 1);
-                if (elect_one()) commit(ms.o_done + slot);
+                if (elect_one()) commit(&ms.o_done);
                 __syncwarp();
             };
             scores(0);
@@ -608,12 +606,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------------ softmax and output
-        const int wg = warp >> 2;
+        // Warps w and w + 4 share TMEM lanes, that is rows: a row's tile is split between two threads, of its first and
+        // its last 64 keys.
+        const int half = warp >> 2;
         const int row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl2 = p.scale * kLog2e;
         const int words = (p.T + 31) / 32;
-        uint32_t s_phase = 0, o_phase = 0;  // bit b: parity of the next phase of buffer / slot b
+        uint32_t s_phase = 0, o_phase = 0;  // s_phase: bit b = parity of the next S in buffer b
         auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
             if (ok) ok = __all_sync(0xffffffffu, bounded_wait(bar, parity));
             tc_fence_after();
@@ -639,75 +639,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t win_end = p.window > 0 ? ctx + w.req.n - p.window : 0;  // keys from here on: no window's edge
             if (end_key > ctx || first_key < win_end) {
                 // (the barrier that ended the last piece keeps its masks from being overwritten)
-                tree_load_parents(p, w.b, w.req.n, ms.par, tid, 256);
+                tree_load_parents(p, w.b, w.req.n, ms.par, tid, kSoftmax);
                 named_bar_sync_256();
-                tree_walk_nodes(p, w.req, node0, min(p.npt, w.req.n - node0), ms.par, anc_s, lo_s, tid, 256);
+                tree_walk_nodes(p, w.req, node0, min(p.npt, w.req.n - node0), ms.par, anc_s, lo_s, tid,
+                                kSoftmax);
                 named_bar_sync_256();
             }
             const bool live_row = row < live;
             const int32_t nd = row / p.Gc;
             const uint32_t* anc = anc_s + nd * words;
-            const int32_t slot = kAlternate ? wg : 0;
-            const uint32_t o_addr = tmem + kOCol + (uint32_t)slot * 128 + lanes;
+            const uint32_t o_addr = tmem + kOCol + lanes;
             const int32_t d_here = min(DV, p.D - st.dv * DV);
-            float m2 = -INFINITY, l = 0.f;
-            bool any = false;  // this slot has had a step in the piece
+            const int32_t d0 = half * (DV / 2), d1 = min(d_here, d0 + DV / 2);  // this thread's share of O's columns
+            float m2 = -INFINITY, l = 0.f;  // the row's maximum, and the sum over this thread's keys
 #pragma unroll 1
-            for (int32_t t = kAlternate ? wg : 0; t < steps && (kAlternate || wg == 0); t += kAlternate ? 2 : 1) {
+            for (int32_t t = 0; t < steps; ++t) {
                 const int buf = t & 1;
                 const int32_t key0 = first_key + t * kTile;
                 const bool edge = key0 + kTile > ctx || key0 < win_end;
                 const uint32_t s_addr = tmem + (uint32_t)buf * 128 + lanes;
                 wait_warp(ms.s_full + buf, (s_phase >> buf) & 1u);
                 s_phase ^= 1u << buf;
-                // keys key0 + 32 c .. + 31 that this row sees
-                auto seen = [&](int c) -> uint32_t {
-                    if (!live_row) return 0u;
-                    const int32_t kb = key0 + 32 * c, a = kb - ctx;
-                    uint32_t bits = bit_span(lo_s[nd] - kb, ctx - kb);
-                    if (a <= -32 || a >= w.req.n) return bits;
-                    if (a < 0) return bits | (anc[0] << -a);
-                    const int wd = a >> 5;
-                    return __funnelshift_r(anc[wd], wd + 1 < words ? anc[wd + 1] : 0u, a & 31) | bits;
-                };
-                // rows of scores in registers, 64 columns at a time: enough independent values to fill the pipes (with
-                // all 128 held across the rescale the compiler spilled)
-                auto load64 = [&](int h, uint32_t (&r)[2][32]) {
-                    tmem_ld32(s_addr + h * 64, r[0]);
-                    tmem_ld32(s_addr + h * 64 + 32, r[1]);
+                uint32_t r[2][32];
+                float mx = -INFINITY;
+                if (ok) {
+                    tmem_ld32(s_addr + half * 64, r[0]);
+                    tmem_ld32(s_addr + half * 64 + 32, r[1]);
                     tmem_ld_wait();
                     reg_fence32(r[0]);
                     reg_fence32(r[1]);
                     if (edge) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const uint32_t bits = seen(2 * h + c);
+                            // keys kb .. kb + 31 that this row sees
+                            const int32_t kb = key0 + half * 64 + 32 * c, a = kb - ctx;
+                            uint32_t bits = 0u;
+                            if (live_row) {
+                                bits = bit_span(lo_s[nd] - kb, ctx - kb);
+                                if (a > -32 && a < 0) {
+                                    bits |= anc[0] << -a;
+                                } else if (a >= 0 && a < w.req.n) {
+                                    const int wd = a >> 5;
+                                    bits |= __funnelshift_r(anc[wd], wd + 1 < words ? anc[wd + 1] : 0u, a & 31);
+                                }
+                            }
 #pragma unroll
                             for (int u = 0; u < 32; ++u) r[c][u] = (bits >> u) & 1u ? r[c][u] : 0xFF800000u;
                         }
                     }
-                };
-                float mx = -INFINITY;
-                if (ok) {
-                    float mc[8];
+                    float mc[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mc[i] = -INFINITY;
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[2][32];
-                        load64(h, r);
+                    for (int i = 0; i < 4; ++i) mc[i] = u2f(r[0][i]);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int u = 0; u < 32; u += 16)
+                        for (int u = c == 0 ? 4 : 0; u + 8 <= 32; u += 8)
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    mc[i] = fmaxf(fmaxf(mc[i], u2f(r[c][u + i])), u2f(r[c][u + 8 + i]));
-                    }
-                    mx = fmaxf(fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])),
-                               fmaxf(fmaxf(mc[4], mc[5]), fmaxf(mc[6], mc[7])));
+                            for (int i = 0; i < 4; ++i)
+                                mc[i] = fmaxf(fmaxf(mc[i], u2f(r[c][u + i])), u2f(r[c][u + 4 + i]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mc[i] = fmaxf(mc[i], u2f(r[0][28 + i]));
+                    mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
                 }
-                mx *= sl2;
+                // Both halves of the row: its maximum, and S is read, so that P may take its place.
+                ms.mx[buf][half][row] = mx;
+                tc_fence_before();
+                named_bar_sync_256();
+                tc_fence_after();
+                mx = fmaxf(mx, ms.mx[buf][half ^ 1][row]) * sl2;
                 const bool grow = live_row && mx > m2 + kRescaleThresh;
                 float alpha = 1.f;
                 if (grow) {
@@ -715,13 +714,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m2 = mx;
                     l *= alpha;
                 }
-                bool waited = false;
-                if (any && __any_sync(0xffffffffu, grow)) {
-                    wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
-                    waited = true;
-                    if (ok) {
+                // (every phase of o_done is waited for once, so that its parity tells them apart)
+                if (t > 0) {
+                    wait_warp(&ms.o_done, o_phase);
+                    o_phase ^= 1u;
+                    if (ok && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
-                        for (int c = 0; c < d_here; c += 16) {
+                        for (int32_t c = d0; c < d1; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(o_addr + c, o);
                             tmem_ld_wait();
@@ -733,91 +732,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st_wait();
                     }
                 }
-                const float mu = m2 == -INFINITY ? 0.f : m2;
-                const uint64_t scale2 = pack2(sl2, sl2), shift2 = pack2(-mu, -mu);
-                uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (ok) {
-                        uint32_t r[2][32];
-                        load64(h, r);
-                        uint32_t pk[2][16];
+                if (half == 1) arrive(ms.p_half + buf);  // its part of O is rescaled
+                if (ok) {
+                    const float mu = m2 == -INFINITY ? 0.f : m2;
+                    const uint64_t scale2 = pack2(sl2, sl2), shift2 = pack2(-mu, -mu);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[16];
 #pragma unroll
-                            for (int u = 0; u < 16; ++u) {
-                                float a, b;
-                                unpack2(fma2(pack2(u2f(r[c][2 * u]), u2f(r[c][2 * u + 1])), scale2, shift2), a, b);
-                                a = ex2(a);
-                                b = ex2(b);
-                                sum[u & 3] = add2(sum[u & 3], pack2(a, b));
-                                const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
-                                pk[c][u] = *reinterpret_cast<const uint32_t*>(&h2);
-                            }
-                        // P over S: columns 32 h .. of the half that is read, and of the first half
-                        tmem_st16(s_addr + h * 32, pk[0]);
-                        tmem_st16(s_addr + h * 32 + 16, pk[1]);
-                        tmem_st_wait();
+                        for (int u = 0; u < 16; ++u) {
+                            float a, b;
+                            unpack2(fma2(pack2(u2f(r[c][2 * u]), u2f(r[c][2 * u + 1])), scale2, shift2), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum[u & 1] = add2(sum[u & 1], pack2(a, b));
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+                            pk[u] = *reinterpret_cast<const uint32_t*>(&h2);
+                        }
+                        tmem_st16(s_addr + half * 32 + c * 16, pk);
                     }
-                    // every phase of o_done is waited for once, so that its parity tells them apart
-                    if (h == 0 && any && !waited) wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
-                    arrive((h == 0 ? ms.p_half : ms.p_full) + buf);
+                    float a, b;
+                    unpack2(add2(sum[0], sum[1]), a, b);
+                    l += a + b;
+                    tmem_st_wait();
                 }
-                if (any) o_phase ^= 1u << slot;
-                any = true;
-                float a, b;
-                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
-                l += a + b;
+                arrive((half == 0 ? ms.p_half : ms.p_full) + buf);
             }
-            if (any) {
-                wait_warp(ms.o_done + slot, (o_phase >> slot) & 1u);
-                o_phase ^= 1u << slot;
-            }
+            wait_warp(&ms.o_done, o_phase);
+            o_phase ^= 1u;
             // ---------------------------------------------------------------- output
             const bool whole = w.whole();
             const int64_t prow = tree_part_row(p, range, sub, w.slot()) + row;
             const int32_t node = node0 + nd, head = w.g * p.G + st.gc * p.Gc + (row - nd * p.Gc);
             const int64_t orow = ((int64_t)w.b * p.T + node) * p.Hq + head;
-            // the row's two accumulators (or one, beside nothing) about their common maximum
             tc_fence_before();
-            ms.m[wg][row] = m2;
-            ms.l[wg][row] = l;
+            ms.l[half][row] = l;
             named_bar_sync_256();
             tc_fence_after();
-            const float ma = ms.m[0][row], mb = ms.m[1][row];
-            const float mm = fmaxf(ma, mb);
-            const float wa = ma == -INFINITY ? 0.f : ex2(ma - mm), wb = mb == -INFINITY ? 0.f : ex2(mb - mm);
-            const float tot = ms.l[0][row] * wa + ms.l[1][row] * wb;
+            const float tot = ms.l[0][row] + ms.l[1][row];
             const float inv = tot > 0.f ? 1.f / tot : 0.f;
-            const float f0 = wa * inv, f1 = wb * inv;
-            if (live_row && wg == 0) {
-                const float lse = tot > 0.f ? (mm + __log2f(tot)) * kLn2 : -INFINITY;
+            if (live_row && half == 0) {
+                const float lse = tot > 0.f ? (m2 + __log2f(tot)) * kLn2 : -INFINITY;
                 if (!whole)
                     p.part_lse[prow] = lse;
                 else if (p.lse && st.dv == 0)
                     p.lse[orow] = lse;
             }
-            // each warpgroup writes half of the columns
-            const int32_t c_begin = wg * (DV / 2), c_end = min(d_here, c_begin + DV / 2);
-            const uint32_t o0 = tmem + kOCol + lanes;
-            const bool second = kAlternate && steps > 1;
+            // each thread writes half of the row's columns
             if (ok) {
 #pragma unroll 1
-                for (int32_t c = c_begin; c < c_end; c += 16) {
+                for (int32_t c = d0; c < d1; c += 16) {
                     uint32_t r[16];
-                    tmem_ld16(o0 + c, r);
+                    tmem_ld16(o_addr + c, r);
                     tmem_ld_wait();
                     reg_fence16(r);
                     float o[16];
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) o[u] = u2f(r[u]) * f0;
-                    if (second) {
-                        tmem_ld16(o0 + 128 + c, r);
-                        tmem_ld_wait();
-                        reg_fence16(r);
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) o[u] = fmaf(u2f(r[u]), f1, o[u]);
-                    }
+                    for (int u = 0; u < 16; ++u) o[u] = u2f(r[u]) * inv;
                     if (!live_row) continue;
                     if (!whole) {
                         float* dst = p.part_out + prow * DV + c;

@@ -306,12 +306,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t key0 = (w.req.tile0 + w.t0 + tile) * kTile;
         return key0 < w.req.lo || key0 + kTile > w.req.L;
     };
-    // zeroes those rows of a V stage (its keys begin at key0); 0 x NaN would reach every row
+    // Zeroes those rows of a V stage (its keys begin at key0); 0 x NaN would reach every row. Boxes without a visible
+    // key came as zeros, so only the rest of the two boxes at the edges is left.
     auto clean = [&](uint8_t* stg, int32_t key0) {
-        for (int idx = lane; idx < kStageBytes / 16; idx += 32) {
-            const int32_t key = key0 + (idx / 8) % kVKeys;
-            if (key < w.req.lo || key >= w.req.L) *reinterpret_cast<uint4*>(stg + idx * 16) = make_uint4(0, 0, 0, 0);
-        }
+        auto zero = [&](int32_t from, int32_t to) {
+            const int32_t r0 = max(from - key0, 0), rows = min(to - key0, kVKeys) - r0;
+            const int32_t slabs = kStageBytes / (kVKeys * 128);
+            for (int32_t idx = lane; idx < rows * 8 * slabs; idx += 32) {
+                const int32_t slab = idx / (rows * 8), rest = idx - slab * rows * 8;
+                *reinterpret_cast<uint4*>(stg + slab * (kVKeys * 128) + (r0 + (rest >> 3)) * 128 + (rest & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+        };
+        zero(w.req.lo & ~(x.box - 1), w.req.lo);
+        zero(w.req.L, (w.req.L + x.box - 1) & ~(x.box - 1));
         fence_proxy_async_smem();
         __syncwarp();
     };
@@ -714,11 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m2 = mx;
                     l *= alpha;
                 }
-                // (every phase of o_done is waited for once, so that its parity tells them apart)
-                if (t > 0) {
+                // O holds the tiles before this one once their product is done: only a rescale waits for it here
+                const bool rescale = t > 0 && __any_sync(0xffffffffu, grow);
+                if (rescale) {
                     wait_warp(&ms.o_done, o_phase);
-                    o_phase ^= 1u;
-                    if (ok && __any_sync(0xffffffffu, grow)) {
+                    if (ok) {
 #pragma unroll 1
                         for (int32_t c = d0; c < d1; c += 16) {
                             uint32_t o[16];
@@ -756,6 +764,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unpack2(add2(sum[0], sum[1]), a, b);
                     l += a + b;
                     tmem_st_wait();
+                }
+                // (every phase of o_done is waited for once, so that its parity tells them apart)
+                if (t > 0) {
+                    if (!rescale) wait_warp(&ms.o_done, o_phase);
+                    o_phase ^= 1u;
                 }
                 arrive((half == 0 ? ms.p_half : ms.p_full) + buf);
             }

@@ -86,7 +86,7 @@ struct TreeAcceptParams {
     int32_t* target_argmax;
     uint32_t* err;
     unsigned long long* keys;  // [B * T], zero between calls
-    int32_t* counters;         // [B], zero between calls
+    unsigned long long* counters;  // [B], zero between calls
 };
 cudaError_t launch_tree_accept(const TreeAcceptParams& p, cudaStream_t stream);
 

@@ -251,7 +251,7 @@ dflash_status dflash_token_logprobs(const void* logits, dflash_dtype dtype, int3
     return DFLASH_OK;
 }
 
-size_t dflash_tree_accept_workspace_bytes(void) { return kKeyBytes + kCounterBytes; }
+size_t dflash_tree_accept_workspace_bytes(void) { return 2 * kKeyBytes; }
 
 dflash_status dflash_tree_accept(const void* logits, dflash_dtype dtype, int32_t batch, int32_t max_nodes,
                                  int32_t vocab, int64_t row_stride, const int32_t* tokens, const int32_t* parents,
@@ -294,7 +294,7 @@ dflash_status dflash_tree_accept(const void* logits, dflash_dtype dtype, int32_t
     p.target_argmax = target_argmax;
     p.err = device_error;
     p.keys = static_cast<unsigned long long*>(workspace);
-    p.counters = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kKeyBytes);
+    p.counters = p.keys + kKeyBytes / sizeof(unsigned long long);
     const cudaError_t e = launch_tree_accept(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tree acceptance kernel launch");
     return DFLASH_OK;

@@ -637,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bar);
             }
         };
+        int32_t masks_of = -1;  // the request whose nodes' masks are in shared memory
         // A failed wait ends the computation, not the walk: the barriers below are met by every thread.
         for (; !w.done(); w.next(p)) {
             if (skip()) continue;
@@ -645,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t ctx = w.req.ctx;
             const int32_t first_key = (w.req.tile0 + w.t0) * kTile, end_key = (w.req.tile0 + w.t1) * kTile;
             const int32_t win_end = p.window > 0 ? ctx + w.req.n - p.window : 0;  // keys from here on: no window's edge
-            if (end_key > ctx || first_key < win_end) {
+            if ((end_key > ctx || first_key < win_end) && masks_of != w.b) {
+                masks_of = w.b;  // (the KV heads of a request share them)
                 // (the barrier that ended the last piece keeps its masks from being overwritten)
                 tree_load_parents(p, w.b, w.req.n, ms.par, tid, kSoftmax);
                 named_bar_sync_256();

@@ -4,8 +4,8 @@
 // Pairs that one range holds whole are final already. A request with a bad length or tree size gets its
 // zeros here.
 //
-// A warp takes a row: its lanes read the partials' lse values (32 at a time) and form the weights, then stream the
-// partial rows, eight loads in flight. Launched as a programmatic dependent of the attention kernel; the deal of
+// A warp takes a row: its lanes read the partials' lse values (32 at a time) and form the weights while the first
+// partial rows come, four or eight a time. Launched as a programmatic dependent of the attention kernel; the deal of
 // tiles to ranges is worked out before the wait for it. Bound: the partials' bytes out of L2.
 #include <algorithm>
 #include <cmath>
@@ -49,57 +49,71 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
     cudaGridDependencySynchronize();
     if (live <= 0 || parts == 1 || (parts == 0 && !rq.bad)) return;
     const int32_t d_here = min(p.DV, p.D - st.dv * p.DV);
-    const int32_t d0 = lane * V;
-    const bool has = d0 < d_here;
+    // A lane's floats: runs of four (two, of 64 dims), 128 dims apart, so that a warp's loads are whole lines.
+    constexpr int kRun = V < 4 ? 2 : 4;
+    const int32_t d0 = lane * kRun;
+    auto dim_of = [&](int u) -> int32_t { return d0 + u / kRun * 128; };  // of run u / kRun
+    const int32_t one = min(parts, 32);
     for (int32_t row = blockIdx.z * kWarps + warp; row < live; row += gridDim.z * kWarps) {
-        float m = -INFINITY;
-        for (int32_t c = lane; c < parts; c += 32)
-            m = fmaxf(m, __ldg(p.part_lse + tree_part_row(p, r0 + c, sub, c == 0 ? 1 : 0) + row));
+        // part c's row: the pair's first part is in slot 1 of its range, the others in slot 0
+        auto part_at = [&](int32_t c) -> int64_t { return tree_part_row(p, r0 + c, sub, c == 0 ? 1 : 0) + row; };
+        auto load = [&](int32_t c, bool live_part, float (&x)[V]) {
+            const float* src = p.part_out + part_at(live_part ? c : 0) * p.DV;
+#pragma unroll
+            for (int u = 0; u < V; u += kRun) {
+                const bool on = live_part && dim_of(u) < d_here;
+                if (V < 4) {
+                    const float2 y = on ? __ldcg(reinterpret_cast<const float2*>(src + dim_of(u))) : make_float2(0.f, 0.f);
+                    x[u] = y.x;
+                    x[u + 1] = y.y;
+                } else {
+                    const float4 y = on ? __ldcg(reinterpret_cast<const float4*>(src + dim_of(u)))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[u] = y.x;
+                    x[u + 1] = y.y;
+                    x[(u + 2) % V] = y.z;
+                    x[(u + 3) % V] = y.w;
+                }
+            }
+        };
+        // The first parts' values are on their way beside the lse values that weigh them: one trip to L2, mostly.
+        constexpr int kAhead = V == 8 ? 8 : 4;
+        float lse0 = -INFINITY, ahead[kAhead][V];
+        if (parts > 0) {
+            lse0 = lane < one ? __ldcg(p.part_lse + part_at(lane)) : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) load(k, k < parts, ahead[k]);
+        }
+        float m = lse0;
+        for (int32_t c = 32 + lane; c < parts; c += 32) m = fmaxf(m, __ldcg(p.part_lse + part_at(c)));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         float t = 0.f, acc[V];
 #pragma unroll
         for (int u = 0; u < V; ++u) acc[u] = 0.f;
         if (m != -INFINITY) {
-            for (int32_t c0 = 0; c0 < parts; c0 += 32) {
-                const int32_t mine = c0 + lane;
-                const float lse = mine < parts
-                                      ? __ldg(p.part_lse + tree_part_row(p, r0 + mine, sub, mine == 0 ? 1 : 0) + row)
-                                      : -INFINITY;
-                const float w = lse == -INFINITY ? 0.f : expf(lse - m);
-                const int32_t here = min(32, parts - c0);
-                for (int32_t c1 = 0; c1 < here; c1 += 8) {
-                    float x[8][V];
+            // (a partial without a visible key is 0 and so is its weight)
+            float w = lse0 == -INFINITY ? 0.f : expf(lse0 - m);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int32_t c = c0 + c1 + k;
-                        const bool on = c1 + k < here && has;
-                        const float* src = p.part_out + (tree_part_row(p, r0 + min(c, parts - 1), sub, c == 0 ? 1 : 0) + row) * p.DV + d0;
+            for (int k = 0; k < kAhead; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);  // 0 past the parts
+                t += wk;
 #pragma unroll
-                        for (int u = 0; u < V; u += V < 4 ? 2 : 4) {
-                            if (V < 4) {
-                                const float2 y = on ? __ldg(reinterpret_cast<const float2*>(src + u)) : make_float2(0.f, 0.f);
-                                x[k][u] = y.x;
-                                x[k][u + 1] = y.y;
-                            } else {
-                                const float4 y = on ? __ldg(reinterpret_cast<const float4*>(src + u))
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-                                x[k][u] = y.x;
-                                x[k][u + 1] = y.y;
-                                x[k][(u + 2) % V] = y.z;
-                                x[k][(u + 3) % V] = y.w;
-                            }
-                        }
-                    }
+                for (int u = 0; u < V; ++u) acc[u] = fmaf(wk, ahead[k][u], acc[u]);
+            }
+            for (int32_t c1 = kAhead; c1 < parts; c1 += kAhead) {
+                if (c1 % 32 == 0) {
+                    const float l = c1 + lane < parts ? __ldcg(p.part_lse + part_at(c1 + lane)) : -INFINITY;
+                    w = l == -INFINITY ? 0.f : expf(l - m);
+                }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        // (a partial without a visible key is 0 and so is its weight)
-                        const float wk = __shfl_sync(0xffffffffu, w, (c1 + k) & 31);
-                        const float wz = c1 + k < here ? wk : 0.f;
-                        t += wz;
+                for (int k = 0; k < kAhead; ++k) load(c1 + k, c1 + k < parts, ahead[k]);
 #pragma unroll
-                        for (int u = 0; u < V; ++u) acc[u] = fmaf(wz, x[k][u], acc[u]);
-                    }
+                for (int k = 0; k < kAhead; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, (c1 + k) & 31);
+                    t += wk;
+#pragma unroll
+                    for (int u = 0; u < V; ++u) acc[u] = fmaf(wk, ahead[k][u], acc[u]);
                 }
             }
         }
@@ -107,17 +121,16 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
         const float inv = empty ? 0.f : 1.f / t;
         const int32_t node = node0 + row / p.Gc, head = g * p.G + st.gc * p.Gc + row % p.Gc;
         const int64_t orow = ((int64_t)b * p.T + node) * p.Hq + head;
-        const int64_t o = orow * p.D + st.dv * p.DV + d0;
-        if (has) {
 #pragma unroll
-            for (int u = 0; u < V; u += 2) {
-                if (p.dtype == DFLASH_BF16)
-                    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + o + u) =
-                        __floats2bfloat162_rn(acc[u] * inv, acc[u + 1] * inv);
-                else
-                    *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o + u) =
-                        make_float2(acc[u] * inv, acc[u + 1] * inv);
-            }
+        for (int u = 0; u < V; u += 2) {
+            const int32_t d = dim_of(u) + u % kRun;
+            if (d >= d_here) continue;
+            const int64_t o = orow * p.D + st.dv * p.DV + d;
+            if (p.dtype == DFLASH_BF16)
+                *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + o) =
+                    __floats2bfloat162_rn(acc[u] * inv, acc[u + 1] * inv);
+            else
+                *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) = make_float2(acc[u] * inv, acc[u + 1] * inv);
         }
         if (lane == 0 && st.dv == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : m + logf(t);
     }

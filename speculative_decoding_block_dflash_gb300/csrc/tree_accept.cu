@@ -2,8 +2,8 @@
 // smallest id among equal maxima) and the walk from the root along the drafted tokens that agree.
 //
 // The argmax is one stream over the real nodes' rows; padding rows are not read. The rows of all requests, laid end to
-// end, are cut into equal parts, one CTA each, four CTAs an SM (one wave): a CTA streams its part, eight 16-byte
-// loads in flight per thread, and settles a row where it ends. (A CTA per 64 KB of a row spent a third of its life in its
+// end, are cut into equal parts, one CTA each, four CTAs an SM (one wave): a CTA streams its part, four to eight
+// 16-byte loads in flight per thread, and settles a row where it ends. (A CTA per 64 KB of a row spent a third of its life in its
 // first load's latency and in the arrival at its end: 53 us for 452 rows of 262144 bf16 logits.) A thread keeps
 // (maximum, first id) in increasing id order, then forms a 64-bit key, the order-preserving image of the value above
 // the complement of the id, so that the largest key is the largest logit of smallest id; -0 is taken as +0 first,
@@ -22,7 +22,7 @@ namespace dflash {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;
+constexpr int kBatch = 4;
 constexpr int kCtasPerSm = 4;
 constexpr int kPartBytes = 8192;  // a CTA's part is this long at least
 
@@ -47,6 +47,12 @@ struct Vec<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
         }
     }
+    static __device__ __forceinline__ float largest(const uint4& w)
+    {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
     static __device__ __forceinline__ float one(const __nv_bfloat16* r, int64_t i) { return __bfloat162float(r[i]); }
 };
 template <>
@@ -58,6 +64,10 @@ struct Vec<float> {
         x[1] = __uint_as_float(w.y);
         x[2] = __uint_as_float(w.z);
         x[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ float largest(const uint4& w)
+    {
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
     static __device__ __forceinline__ float one(const float* r, int64_t i) { return r[i]; }
 };
@@ -157,10 +167,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_accept_kernel(const
                 bi = more ? id : bi;
             };
             auto take_vec = [&](const uint4& w, int32_t id) {
+                // a vector whose largest value does not exceed the running one (nearly all) costs four maxima
+                const float most = V::largest(w);
+                if (!(most > bv || bi < 0)) return;
                 float x[V::kN];
                 V::widen(w, x);
+                int first = 0;
 #pragma unroll
-                for (int e = 0; e < V::kN; ++e) take(x[e], id + e);
+                for (int e = V::kN - 1; e >= 0; --e)
+                    if (x[e] == most) first = e;
+                bv = most;
+                bi = id + first;
             };
             auto id_of = [&](int32_t q) { return (int32_t)((uint32_t)q * V::kN - mis); };
             // vectors at the row's ends that hold other elements too are read element by element
@@ -178,23 +195,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_accept_kernel(const
                 q += kThreads;
             }
             const int32_t qw = min(q1, whole1);
-            for (; q + (kBatch - 1) * kThreads < qw; q += kBatch * kThreads) {
-                uint4 w[kBatch];
+            uint4 cur[kBatch], nxt[kBatch];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) w[u] = load(q + u * kThreads);
+            for (int u = 0; u < kBatch; ++u)
+                if (q + u * kThreads < qw) cur[u] = load(q + u * kThreads);
+#pragma unroll 1
+            while (q + (2 * kBatch - 1) * kThreads < qw) {
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) take_vec(w[u], id_of(q + u * kThreads));
+                for (int u = 0; u < kBatch; ++u) nxt[u] = load(q + (kBatch + u) * kThreads);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) take_vec(cur[u], id_of(q + u * kThreads));
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) cur[u] = nxt[u];
+                q += kBatch * kThreads;
             }
-            {
-                uint4 w[kBatch];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    if (q + u * kThreads < qw) w[u] = load(q + u * kThreads);
+            for (int u = 0; u < kBatch; ++u)
+                if (q + (kBatch + u) * kThreads < qw) nxt[u] = load(q + (kBatch + u) * kThreads);
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    if (q + u * kThreads < qw) take_vec(w[u], id_of(q + u * kThreads));
-                while (q < qw) q += kThreads;
-            }
+            for (int u = 0; u < kBatch; ++u)
+                if (q + u * kThreads < qw) take_vec(cur[u], id_of(q + u * kThreads));
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (q + (kBatch + u) * kThreads < qw) take_vec(nxt[u], id_of(q + (kBatch + u) * kThreads));
+            while (q < qw) q += kThreads;
             if (q < q1) take_part(q);  // the last vector, if it is not whole
             unsigned long long best = bi >= 0 ? make_key(bv, (uint32_t)bi) : 0ull;
 #pragma unroll

@@ -6,20 +6,22 @@
 // differences stay exact to fp32 whatever the size of the logits, and a row with one likely token keeps its
 // small entropy.
 //
-// A row is cut into slices, a CTA of 128 threads each, read in steps of 16 values a thread with the next step's
-// loads in flight. A step's values stay in registers for everything: the maximum, the sums and the selection.
+// A row is cut into slices, a CTA of 128 threads each, streamed in steps of 16 values a thread with the next step's
+// loads in flight; no barrier until its end. Beside the sums a thread keeps the maximum of each sixteenth of its
+// steps: of a group of values.
 //
 // Selection. A value and its id form a 64-bit key (order-preserving image of the value above the id's
-// complement), all distinct, so "the k largest keys" is the definition. A CTA keeps its k largest so far, and a bound
-// that every key still in the running exceeds. A thread looks for candidates only in steps whose maximum reaches the
-// bound's value, and forms keys only of the values that do. In the first step, where all do, the thread maxima give a
-// bound: sorted within each warp (shuffles), the least of the four warps' ceil(k / 4)-th largest has k maxima at or above
-// it. From then on the warps run on their own in rounds of 1, 2, 4, ... steps; a warp adds its candidates to the
-// buffer, and at a round's end they and the kept keys are ranked against each other (a key's rank is the number of
-// larger ones; no sort), the first k stay, and the bound follows. Each round doubles what has been seen, so on usual
-// data it adds about k candidates, and a row has few barriers. A warp whose share of the buffer could overflow ends its
-// round early: nothing but the time depends on the data. (Per-step barriers, a sort of 256 per merge and keys formed for
-// every value of a warp with a candidate: 460 us for 1000 rows of 151937; barriers and ranks: 148.)
+// complement), all distinct, so "the k largest keys" is the definition. At the slice's end the threads' maxima give a
+// bound: sorted within each warp (shuffles), the least of the four warps' ceil(k / 4)-th largest has k values at or
+// above it. Only groups whose maximum reaches it are read again (some 70 to 100 of 2048 for k = 64, four percent of a
+// row of 152k), and only their values that reach it become candidates. Candidates and kept keys are ranked
+// against each other (a key's rank is the number of larger ones; no sort) and the first k stay. The buffer holds 256
+// candidates of each warp; a warp that might add more waits for a merge, so nothing but the time depends on the
+// data: a row of equal logits reads every group again.
+// A thread's values of a step are whole sectors, so that reading a group again fetches little beside it. Measured, k = 64
+// beside none: 1000 rows of 151937 fp32 137 and 107 us (floor 90), bf16 88 and 66 (45); 4000 rows of 32000 bf16 100
+// and 61 (38). (Candidates picked step by step, with a sort of 256 per merge, took 460 us for the first, with merges by
+// rank at every doubling of what has been seen 143; and 190 for the last: merges, not the stream, took the time.)
 //
 // Slices leave their sums and keys in the workspace; the last CTA of a row to arrive (a counter, no waiting) merges
 // them the same way and writes the row.
@@ -37,8 +39,9 @@ constexpr int kElems = 16;      // values per thread and step
 constexpr int kCtasPerSm = 8;
 constexpr int kSliceElems = 2048;  // a step: the shortest slice
 constexpr int kMaxK = DFLASH_MAX_TOP_K;
-constexpr int kWarpRoom = 32 * kElems;             // candidates a warp may add in a round: a step's at least
-constexpr int kCand = kThreads / 32 * kWarpRoom;
+constexpr int kWarpRoom = 256;  // candidates a warp may add between merges: 32 vectors of bf16 at least
+constexpr int kCand = kThreads / 32 * kWarpRoom + 512;  // what may wait, and what may come before it is looked at
+constexpr int kAgain = 4;  // vectors read again at once, per thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -97,12 +100,23 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
+constexpr int kPhases = 16;  // groups per thread
+
+// (17 KB a CTA: with 25 KB, eight to an SM, the loads in flight had too little of the L1 left: 104 -> 133 us without
+// top tokens.)
 struct Shared {
-    Key keys[kMaxK + kCand];  // the kept ones, largest first, then the waiting candidates
+    Key kept[kMaxK];  // the k largest so far, largest first
+    union {
+        float group[kPhases][kThreads];  // maxima, until the groups to read again are listed
+        Key cand[kCand];                 // then the waiting candidates
+    };
+    uint16_t list[kPhases * kThreads];  // groups to read again: phase * kThreads + thread
+    int32_t n_list;
     Key warp_key[kThreads / 32];
     Key bound;                // keys at or below it are out
     int32_t n_kept, n_cand;
     int32_t last;
+    float warp_top[kThreads / 32];
     float red[3][kThreads / 32];
 };
 
@@ -111,21 +125,21 @@ __device__ __forceinline__ void merge(Shared& sh, int32_t k, int tid)
 {
     const int32_t n_cand = sh.n_cand;
     int32_t kept = sh.n_kept;
-    Key* cand = sh.keys + kMaxK;
+    const Key* cand = sh.cand;
 #pragma unroll 1
     for (int32_t at = 0; at < n_cand; at += kThreads - kMaxK) {
         const int32_t here = min(n_cand - at, kThreads - kMaxK);
         Key mine = 0;
         int32_t rank = 0;
         if (tid < kept) {
-            mine = sh.keys[tid];
+            mine = sh.kept[tid];
             rank = tid;
         } else if (tid >= kMaxK && tid - kMaxK < here) {
             mine = cand[at + tid - kMaxK];
             int32_t lo = 0, hi = kept;  // kept keys are in order
             while (lo < hi) {
                 const int32_t mid = (lo + hi) >> 1;
-                if (sh.keys[mid] > mine)
+                if (sh.kept[mid] > mine)
                     lo = mid + 1;
                 else
                     hi = mid;
@@ -137,31 +151,33 @@ __device__ __forceinline__ void merge(Shared& sh, int32_t k, int tid)
             for (int32_t i = 0; i < here; ++i) rank += cand[at + i] > mine;
         }
         __syncthreads();
-        if (mine && rank < k) sh.keys[rank] = mine;
+        if (mine && rank < k) sh.kept[rank] = mine;
         kept = min(k, kept + here);
         __syncthreads();
     }
     if (tid == 0) {
         sh.n_cand = 0;
         sh.n_kept = kept;
-        if (kept == k) sh.bound = max(sh.bound, sh.keys[k - 1]);
+        if (kept == k) sh.bound = max(sh.bound, sh.kept[k - 1]);
     }
     __syncthreads();
 }
 
-// The j-th largest (from 0) of a warp's keys.
-__device__ __forceinline__ Key warp_nth(Key k, int j, int lane)
+// The j-th largest (from 0) of a warp's values.
+template <typename T>
+__device__ __forceinline__ T warp_nth(T x, int j, int lane)
 {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1) {
         const bool down = (lane & size) == 0;
 #pragma unroll
         for (int d = size >> 1; d > 0; d >>= 1) {
-            const Key other = __shfl_xor_sync(0xffffffffu, k, d);
-            k = (((lane & d) == 0) == down) ? max(k, other) : min(k, other);
+            const T other = __shfl_xor_sync(0xffffffffu, x, d);
+            const bool larger = ((lane & d) == 0) == down;  // this lane takes the larger of the two
+            x = larger ? (x > other ? x : other) : (x > other ? other : x);
         }
     }
-    return __shfl_sync(0xffffffffu, k, j);
+    return __shfl_sync(0xffffffffu, x, j);
 }
 
 // A bound from one key of each thread's (0: none), its largest: at least k keys exceed it, or it is the old one.
@@ -178,7 +194,119 @@ __device__ __forceinline__ void raise_bound(Shared& sh, int32_t k, int tid, Key 
     __syncthreads();
 }
 
-__device__ __forceinline__ void put(Shared& sh, Key key) { sh.keys[kMaxK + atomicAdd(&sh.n_cand, 1)] = key; }
+__device__ __forceinline__ void put(Shared& sh, Key key) { sh.cand[atomicAdd(&sh.n_cand, 1)] = key; }
+
+// Element e of a 16-byte vector of E.
+template <typename E>
+__device__ __forceinline__ float element(const uint4& v, int e)
+{
+    if (sizeof(E) == 2) {
+        const uint32_t x = e / 2 == 0 ? v.x : e / 2 == 1 ? v.y : e / 2 == 2 ? v.z : v.w;
+        return __uint_as_float(e % 2 ? x & 0xFFFF0000u : x << 16);
+    }
+    return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+}
+
+struct Slice {
+    const void* base;         // its first sector
+    int32_t nq;               // sectors (32 bytes)
+    int32_t whole0, whole1;   // those that hold the row's elements only
+    int32_t id0;              // id of the first element
+    int32_t steps, phase_len;
+};
+
+// The k largest keys of the slice whose group maxima are in sh.group. Out of line: the stream keeps its registers.
+template <typename E>
+__device__ __noinline__ void select_again(Shared& sh, int32_t k, const Slice sl, float top, bool has_edge, float edge_x,
+                                          int32_t edge_id)
+{
+    constexpr int kN = 16 / sizeof(E);
+    constexpr int kVecs = kElems / kN;
+    constexpr int kSecs = kVecs / 2;
+    const int tid = threadIdx.x;
+    // the bound: a value that k values or more reach (-inf where there are not that many)
+    const float nth = warp_nth(top, (k + kThreads / 32 - 1) / (kThreads / 32) - 1, tid & 31);
+    if ((tid & 31) == 0) sh.warp_top[tid >> 5] = nth;
+    __syncthreads();
+    float limit = sh.warp_top[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) limit = fminf(limit, sh.warp_top[i]);
+    for (int32_t phase = 0; phase * sl.phase_len < sl.steps; ++phase)
+        if (sh.group[phase][tid] >= limit) sh.list[atomicAdd(&sh.n_list, 1)] = (uint16_t)(phase * kThreads + tid);
+    __syncthreads();  // the groups' maxima make room for candidates
+    if (has_edge && edge_x >= limit) put(sh, make_key(edge_x, (uint32_t)edge_id));
+    // the groups' 16-byte vectors, a group's `per` one after another, dealt to the threads four at a time
+    const int32_t per = sl.phase_len * kVecs;
+    const int64_t total = (int64_t)sh.n_list * per;
+    Key bound = 0;
+    int64_t from = 0;
+#pragma unroll 1
+    do {
+        uint4 v[kAgain];
+        int32_t at[kAgain];  // 16-byte vector of the slice, or -1
+#pragma unroll
+        for (int i = 0; i < kAgain; ++i) {
+            const int64_t j = from + i * kThreads + tid;
+            at[i] = -1;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (j < total) {
+                const int32_t e = total <= INT32_MAX ? (int32_t)j / per : (int32_t)(j / per);
+                const int32_t g = sh.list[e], vec = g / kThreads * per + (int32_t)(j - (int64_t)e * per);
+                const int32_t q = (vec >> 1) * kThreads + g % kThreads;  // its sector
+                if ((vec >> 1) < sl.steps * kSecs && q >= sl.whole0 && q < sl.whole1) {
+                    at[i] = 2 * q + (vec & 1);
+                    v[i] = __ldg(static_cast<const uint4*>(sl.base) + at[i]);
+                }
+            }
+        }
+        from += kAgain * kThreads;
+        int done = 0;  // vectors of this warp that are through
+        bool again;
+#pragma unroll 1
+        do {
+            int32_t room = kWarpRoom;
+#pragma unroll 1
+            for (; done < kAgain; ++done) {
+                uint4 x = v[0];
+                int32_t q = at[0];
+#pragma unroll
+                for (int i = 1; i < kAgain; ++i)
+                    if (done == i) {
+                        x = v[i];
+                        q = at[i];
+                    }
+                float most = element<E>(x, 0);
+#pragma unroll
+                for (int e = 1; e < kN; ++e) most = fmaxf(most, element<E>(x, e));
+                const bool hot = q >= 0 && most >= limit;
+                const uint32_t who = __ballot_sync(0xffffffffu, hot);
+                if (who == 0) continue;
+                if (__popc(who) * kN > room) break;  // the rest after a merge
+                int n = 0;
+                if (hot) {
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) {
+                        if (!(element<E>(x, e) >= limit)) continue;
+                        const Key key = make_key(element<E>(x, e), (uint32_t)(sl.id0 + q * kN + e));
+                        if (key > bound) {
+                            put(sh, key);
+                            ++n;
+                        }
+                    }
+                }
+                room -= __reduce_add_sync(0xffffffffu, n);
+            }
+            again = __syncthreads_or(done < kAgain) != 0;
+            const bool full = sh.n_cand > kCand - kThreads / 32 * kWarpRoom;
+            __syncthreads();
+            if (full || (!again && from >= total)) {
+                merge(sh, k, tid);
+                bound = sh.bound;
+                if (bound) limit = fmaxf(limit, key_value(bound));
+            }
+        } while (again);
+    } while (from < total);
+}
 
 // A shift of the maximum in the exponent. 2^-200 is 0; a longer shift would only make the products with it
 // infinite.
@@ -201,28 +329,28 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float& w, float m
 template <typename E>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(const LogprobsParams p)
 {
-    constexpr int kN = 16 / sizeof(E);
-    constexpr int kVecs = kElems / kN;
+    constexpr int kN = 32 / sizeof(E);  // elements of a sector
+    constexpr int kSecs = kElems / kN;  // sectors per thread and step
     __shared__ Shared sh;
     const int tid = threadIdx.x;
     const int32_t row = blockIdx.y;
     const int32_t k = p.k;
     const E* r = static_cast<const E*>(p.logits) + row * p.row_stride;
-    // The row in 16-byte vectors, counted from the boundary at or before its first element. This CTA's are [q0, q1);
-    // those at the row's ends that hold other elements too are read element by element. Offsets within the slice
-    // fit 32 bits.
-    const int32_t mis = (int32_t)((reinterpret_cast<uintptr_t>(r) & 15) / sizeof(E));
-    const int64_t vecs = ((int64_t)p.V + mis + kN - 1) / kN;
-    const int64_t per = (vecs + p.slices - 1) / p.slices;
-    const int64_t q0 = min(vecs, blockIdx.x * per);
-    const int32_t nq = (int32_t)(min(vecs, q0 + per) - q0);
+    // The row in sectors of 32 bytes, counted from the boundary at or before its first element. This CTA's are
+    // [q0, q0 + nq); those at the row's ends that hold other elements too ([0, whole0) and [whole1, nq)) are read
+    // element by element. Offsets within the slice fit 32 bits.
+    const int32_t mis = (int32_t)((reinterpret_cast<uintptr_t>(r) & 31) / sizeof(E));
+    const int64_t secs = ((int64_t)p.V + mis + kN - 1) / kN;
+    const int64_t per = (secs + p.slices - 1) / p.slices;
+    const int64_t q0 = min(secs, blockIdx.x * per);
+    const int32_t nq = (int32_t)(min(secs, q0 + per) - q0);
     const int32_t whole0 = q0 == 0 && mis ? 1 : 0;
-    const int32_t whole1 = q0 + nq == vecs && (p.V + mis) % kN ? nq - 1 : nq;
+    const int32_t whole1 = q0 + nq == secs && (p.V + mis) % kN ? nq - 1 : nq;
     const E* base = r + (q0 * kN - mis);
     const int32_t id0 = (int32_t)(q0 * kN) - mis;  // id of the slice's first element
     const float sl2 = kLog2e / p.temperature;
     if (tid == 0) {
-        sh.n_kept = sh.n_cand = 0;
+        sh.n_kept = sh.n_cand = sh.n_list = 0;
         sh.bound = 0;
     }
     // a given token's logit, fetched while the row streams
@@ -236,145 +364,112 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     }
     __syncthreads();
 
-    // Values outside the row count as -inf without a key.
-    auto fetch = [&](int32_t at, uint4 (&raw)[kVecs]) {
-        const uint4* src = reinterpret_cast<const uint4*>(base) + at + tid;
-        if (at >= whole0 && at + kVecs * kThreads <= whole1) {
-#pragma unroll
-            for (int u = 0; u < kVecs; ++u) raw[u] = __ldcs(src + u * kThreads);
-            return;
+    // The elements of those vectors at the ends: one of a thread's first few.
+    bool has_edge = false;
+    float edge_x = -INFINITY;
+    int32_t edge_id = 0;
+    if (tid < 2 * kN && nq > 0) {
+        const bool tail = tid >= kN;
+        const bool here = tail ? whole1 < nq && nq - 1 >= whole0 : whole0 > 0;
+        const int64_t id = (q0 + (tail ? nq - 1 : 0)) * kN - mis + tid % kN;
+        has_edge = here && id >= 0 && id < p.V;
+        if (has_edge) {
+            edge_id = (int32_t)id;
+            edge_x = sizeof(E) == 2 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(r)[id])
+                                    : reinterpret_cast<const float*>(r)[id];
         }
+    }
+
+    // Sectors that are not the slice's count as -inf.
+    auto fetch = [&](int32_t at, uint4 (&raw)[2 * kSecs]) {
+        const bool all = at >= whole0 && at + kSecs * kThreads <= whole1;
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
+        for (int u = 0; u < kSecs; ++u) {
             const int32_t q = at + u * kThreads + tid;
             const uint32_t none = sizeof(E) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
-            raw[u] = make_uint4(none, none, none, none);
-            if (q >= whole0 && q < whole1) {
-                raw[u] = __ldcs(src + u * kThreads);
-            } else if (q < nq) {
-                E* part = reinterpret_cast<E*>(&raw[u]);
-#pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    const int64_t id = (q0 + q) * kN - mis + e;
-                    if (id >= 0 && id < p.V) part[e] = r[id];
-                }
+            if (all || (q >= whole0 && q < whole1)) {
+                const uint4* src = reinterpret_cast<const uint4*>(base) + 2 * (int64_t)q;
+                raw[2 * u] = __ldcs(src);
+                raw[2 * u + 1] = __ldcs(src + 1);
+            } else {
+                raw[2 * u] = raw[2 * u + 1] = make_uint4(none, none, none, none);
             }
         }
     };
-    auto value = [&](const uint4 (&raw)[kVecs], int i) -> float {
-        const uint4& v = raw[i / kN];
-        const int e = i % kN;
+    auto value = [&](const uint4 (&raw)[2 * kSecs], int i) -> float {
+        return element<E>(raw[i / (kN / 2)], i % (kN / 2));
+    };
+    auto step_max = [&](const uint4 (&raw)[2 * kSecs]) -> float {
         if (sizeof(E) == 2) {
-            const uint32_t w = e / 2 == 0 ? v.x : e / 2 == 1 ? v.y : e / 2 == 2 ? v.z : v.w;
-            return __uint_as_float(e % 2 ? w & 0xFFFF0000u : w << 16);
+            // pairs of bf16 as they lie
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw[0]);
+            __nv_bfloat162 x = h[0];
+#pragma unroll
+            for (int i = 1; i < kElems / 2; ++i) x = __hmax2(x, h[i]);
+            return fmaxf(__low2float(x), __high2float(x));
         }
-        return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+        float x = value(raw, 0);
+#pragma unroll
+        for (int i = 1; i < kElems; ++i) x = fmaxf(x, value(raw, i));
+        return x;
     };
 
     float m = -INFINITY, s = 0.f, w = 0.f;
-    uint4 cur[kVecs], nxt[kVecs];
-    fetch(0, cur);
-    int32_t at = 0;  // this warp's step
-    float mq[kElems / 4], mt;
-    // maxima of four values each, and of the step
-    auto maxima = [&]() {
-        mt = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kElems / 4; ++i) {
-            mq[i] = fmaxf(fmaxf(value(cur, 4 * i), value(cur, 4 * i + 1)), fmaxf(value(cur, 4 * i + 2), value(cur, 4 * i + 3)));
-            mt = fmaxf(mt, mq[i]);
-        }
-    };
-    // one of the thread's keys in this step, of its largest value
-    auto any_key = [&]() -> Key {
-        // (a thread of nothing but -inf: the first value of its first vector that lies in the row)
-        int first = 0;
-#pragma unroll
-        for (int i = kElems - 1; i >= 0; --i)
-            if (value(cur, i) == mt && mt > -INFINITY) first = i;
-        const int32_t id = id0 + (at + (first / kN) * kThreads + tid) * kN + first % kN;
-        return at + tid < nq ? make_key(mt, (uint32_t)max(id, 0)) : 0;
-    };
-    // hands the step's keys above the bound to the buffer; how many
-    auto push = [&](Key above) -> int {
-        const float least = above ? key_value(above) : -INFINITY;
-        int n = 0;
-#pragma unroll
-        for (int g = 0; g < kElems / 4; ++g) {
-            if (!(mq[g] >= least)) continue;
-#pragma unroll
-            for (int i = 4 * g; i < 4 * g + 4; ++i)
-                if (value(cur, i) >= least) {
-                    const int32_t q = at + (i / kN) * kThreads + tid;
-                    const int32_t id = id0 + q * kN + i % kN;
-                    const bool in = (q >= whole0 && q < whole1) || (q < nq && id >= 0 && id < p.V);
-                    const Key key = make_key(value(cur, i), (uint32_t)id);
-                    if (in && key > above) {
-                        put(sh, key);
-                        ++n;
-                    }
-                }
-        }
-        return n;
-    };
-    Key bound = 0;
-    if (k > 0) {
-        maxima();
-        raise_bound(sh, k, tid, any_key());
-        bound = sh.bound;
+    const int32_t steps = (nq + kSecs * kThreads - 1) / (kSecs * kThreads);
+    const int32_t phase_len = max(1, (steps + kPhases - 1) / kPhases);
+    float top = edge_x;  // the thread's largest value
+    if (edge_x > -INFINITY) {
+        m = edge_x;
+        s = 1.f;
     }
+    {
+        uint4 cur[2 * kSecs], nxt[2 * kSecs];
+        fetch(0, cur);
+        int32_t step = 0;
 #pragma unroll 1
-    for (int32_t len = 1;; len = min(2 * len, 1 << 20)) {
-        int32_t room = kWarpRoom;
+        for (int32_t phase = 0; step < steps; ++phase) {
+            const int32_t end = min(steps, step + phase_len);
+            float group = -INFINITY;
 #pragma unroll 1
-        for (int32_t todo = len; todo > 0 && at < nq; --todo) {
-            maxima();
-            if (k > 0) {
-                const bool hot = at + tid < nq && (bound == 0 || mt >= key_value(bound));
-                const uint32_t who = __ballot_sync(0xffffffffu, hot);
-                if (who) {
-                    if (__popc(who) * kElems > room) break;
-                    room -= __reduce_add_sync(0xffffffffu, hot ? push(bound) : 0);
+            for (; step < end; ++step) {
+                if (step + 1 < steps) fetch((step + 1) * kSecs * kThreads, nxt);
+                const float mt = step_max(cur);
+                group = fmaxf(group, mt);
+                if (mt > m) {
+                    const float d = shift(m, mt, sl2);
+                    const float a = ex2(d);
+                    w = (w + d * s) * a;
+                    s *= a;
+                    m = mt;
                 }
-            }
-            at += kVecs * kThreads;
-            if (at < nq) fetch(at, nxt);
-            if (mt > m) {
-                const float d = shift(m, mt, sl2);
-                const float a = ex2(d);
-                w = (w + d * s) * a;
-                s *= a;
-                m = mt;
-            }
-            const float mu = m == -INFINITY ? 0.f : m;
-            const uint64_t neg2 = pack2(-mu, -mu), scale2 = pack2(sl2, sl2);
-            uint64_t s2 = 0, w2 = 0;
+                const float mu = m == -INFINITY ? 0.f : m;
+                const uint64_t neg2 = pack2(-mu, -mu), scale2 = pack2(sl2, sl2);
+                uint64_t s2 = 0, w2 = 0;
 #pragma unroll
-            for (int i = 0; i < kElems; i += 2) {
-                // a value of -inf has no share: 2^-200 is 0, and y stays finite for the entropy's product
-                float y0, y1;
-                unpack2(mul2(add2(pack2(value(cur, i), value(cur, i + 1)), neg2), scale2), y0, y1);
-                y0 = fmaxf(y0, -200.f);
-                y1 = fmaxf(y1, -200.f);
-                const uint64_t e2 = pack2(ex2(y0), ex2(y1));
-                s2 = add2(s2, e2);
-                w2 = fma2(pack2(y0, y1), e2, w2);
-            }
-            float a0, a1;
-            unpack2(s2, a0, a1);
-            s += a0 + a1;
-            unpack2(w2, a0, a1);
-            w += a0 + a1;
+                for (int i = 0; i < kElems; i += 2) {
+                    // a value of -inf has no share: 2^-200 is 0, and y stays finite for the entropy's product
+                    float y0, y1;
+                    unpack2(mul2(add2(pack2(value(cur, i), value(cur, i + 1)), neg2), scale2), y0, y1);
+                    y0 = fmaxf(y0, -200.f);
+                    y1 = fmaxf(y1, -200.f);
+                    const uint64_t e2 = pack2(ex2(y0), ex2(y1));
+                    s2 = add2(s2, e2);
+                    w2 = fma2(pack2(y0, y1), e2, w2);
+                }
+                float a0, a1;
+                unpack2(s2, a0, a1);
+                s += a0 + a1;
+                unpack2(w2, a0, a1);
+                w += a0 + a1;
 #pragma unroll
-            for (int u = 0; u < kVecs; ++u) cur[u] = nxt[u];
+                for (int u = 0; u < 2 * kSecs; ++u) cur[u] = nxt[u];
+            }
+            sh.group[phase][tid] = group;
+            top = fmaxf(top, group);
         }
-        const bool more = __syncthreads_or(at < nq) != 0;
-        if (k > 0) {
-            merge(sh, k, tid);  // (ends with a barrier, past which the next candidates come)
-            bound = sh.bound;
-        }
-        if (!more) break;
     }
+    if (k > 0)
+        select_again<E>(sh, k, Slice{base, nq, whole0, whole1, id0, steps, phase_len}, top, has_edge, edge_x, edge_id);
     // the CTA's sums
     auto reduce_stats = [&]() {
 #pragma unroll
@@ -404,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
             st[1] = s;
             st[2] = w;
         }
-        if (tid < k) p.part_key[part * k + tid] = tid < sh.n_kept ? sh.keys[tid] : 0;
+        if (tid < k) p.part_key[part * k + tid] = tid < sh.n_kept ? sh.kept[tid] : 0;
         __threadfence();
         __syncthreads();
         if (tid == 0) sh.last = atomicAdd(p.counters + row, 1) == p.slices - 1;
@@ -436,20 +531,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
                 top = __ldcg(keys + (int64_t)(tid % p.slices) * k + tid / p.slices);
             }
             raise_bound(sh, k, tid, top);
-            for (int64_t at = 0; at < total; at += 8 * kThreads) {
+            for (int64_t at = 0; at < total; at += 4 * kThreads) {
                 const Key bound = sh.bound;
-                Key mine[8];
+                Key mine[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     const int64_t j = at + i * kThreads + tid;
                     mine[i] = j < total ? __ldcg(keys + j) : 0;
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 4; ++i)
                     if (mine[i] > bound) put(sh, mine[i]);
-                const bool last = at + 8 * kThreads >= total;
+                const bool last = at + 4 * kThreads >= total;
                 __syncthreads();
-                const bool full = sh.n_cand > kCand - 8 * kThreads;
+                const bool full = sh.n_cand > kCand - 4 * kThreads;
                 __syncthreads();
                 if (full || last) merge(sh, k, tid);
             }
@@ -473,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
         p.token_logp[(int64_t)row * p.m + tid] = out;
     }
     if (tid < k) {
-        const Key key = tid < sh.n_kept ? sh.keys[tid] : 0;  // all k are there, unless the row holds NaN
+        const Key key = tid < sh.n_kept ? sh.kept[tid] : 0;  // all k are there, unless the row holds NaN
         p.top_tokens[(int64_t)row * k + tid] = key_id(key);
         p.top_logp[(int64_t)row * k + tid] = logp(key_value(key));
     }

@@ -498,14 +498,16 @@ DFLASH_API dflash_status dflash_token_logprobs(const void* logits, dflash_dtype 
  *   parents       device, int32 [B, max_nodes]; num_nodes device int32 [B] or NULL.
  *   dims          as in dflash_block_attn; max_nodes = T in [1, DFLASH_MAX_TREE_NODES].
  *   window        0 or W >= 1; scale finite and > 0.
- *   out           device, [B*T, Hq, D] contiguous, dims->dtype; padding rows are left as they were.
+ *   out           device, [B*T, Hq, D] contiguous, dims->dtype; padding rows are left as they were. No output
+ *                 may overlap an input.
  *   lse           device, float32 [B*T, Hq] or NULL; padding rows are left as they were.
  *   kernel        DFLASH_KERNEL_AUTO, DFLASH_KERNEL_SIMT (CUDA cores; fp32 and every shape) or DFLASH_KERNEL_TC
  *                 (tensor cores; bf16). AUTO takes TC for bf16 where it covers the layout (every
  *                 page size of the contract; strides of the cache > 0).
  *   workspace     device, 256-byte aligned, dflash_tree_attn_workspace_bytes() long for the current
  *                 device: the error word (256 bytes, zeroed once before its first use; read with
- *                 dflash_read_error), then the partial results of split key ranges.
+ *                 dflash_read_error), 8 KB that dflash_read_error may clear, then the partial
+ *                 results of split key ranges.
  *   wait_limit_us as in dflash_opts.
  * A seq_len outside [n_b, max_seq_len] (DFLASH_DEVERR_SEQ_LEN) or a tree size outside [0, T]
  * (DFLASH_DEVERR_TREE) makes the request's T rows zeros with lse = -inf. An out-of-range page id

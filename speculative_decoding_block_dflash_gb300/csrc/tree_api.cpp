@@ -46,9 +46,10 @@ struct TreeAttnLayout {
 
 TreeAttnLayout tree_attn_layout(const TreeAttnParams& p)
 {
-    const size_t rows = (size_t)p.ranges * p.n_sub * 2 * p.rows;
+    // nothing is split when every query tile has but one range
+    const size_t rows = p.ranges > 1 ? (size_t)p.ranges * p.n_sub * 2 * p.rows : 0;
     TreeAttnLayout w;
-    w.lse_off = 256;
+    w.lse_off = 256 + DFLASH_COUNTER_BYTES;  // (dflash_read_error clears as much after a timeout)
     w.out_off = w.lse_off + round_up(rows * sizeof(float), 256);
     w.total = w.out_off + round_up(rows * p.DV * sizeof(float), 256);
     return w;
@@ -147,6 +148,7 @@ dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v
         return report_error(DFLASH_ERR_INVALID_ARG, "NULL tensor pointer");
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
         return report_error(DFLASH_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
+    if (out == q) return report_error(DFLASH_ERR_INVALID_ARG, "out must not alias q");
     if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(num_nodes, 4) ||
         !aligned(lse, 4))
         return report_error(DFLASH_ERR_INVALID_ARG, "page_table, seq_lens, parents, num_nodes and lse must be 4-byte aligned");

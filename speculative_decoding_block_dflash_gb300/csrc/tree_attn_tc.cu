@@ -64,7 +64,10 @@ constexpr int kStageBytes = 16384;
 constexpr int kMaxStages = 13;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kOCol = 256;  // first TMEM column of O
-constexpr unsigned long long kCopyGraceNs = 200000ull;  // after a failed wait: time for copies in flight to land
+// After a failed wait, whatever the caller's limit: the bound of the waits for copies and MMAs in flight, and the time given
+// to copies that this CTA cannot wait for.
+constexpr unsigned long long kDrainNs = 100000000ull;
+constexpr unsigned long long kCopyGraceNs = 1000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThresh = 8.0f;
@@ -445,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) {
                 for (int s = 0; s < S; ++s)
                     if (issued & (1u << s))
-                        while (!mbar_test_wait(ms.full + s, (issued_phase >> s) & 1u) && globaltimer() - t0 < p.wait_ns) {
+                        while (!mbar_test_wait(ms.full + s, (issued_phase >> s) & 1u) && globaltimer() - t0 < kDrainNs) {
                         }
                 if (q_out)
-                    while (!mbar_test_wait(&ms.q_full, q_phase ^ 1u) && globaltimer() - t0 < p.wait_ns) {
+                    while (!mbar_test_wait(&ms.q_full, q_phase ^ 1u) && globaltimer() - t0 < kDrainNs) {
                     }
             }
             if (kPair)
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
                 tc_commit(&ms.drain);
             const unsigned long long t0 = globaltimer();
-            while (!mbar_test_wait(&ms.drain, 0) && globaltimer() - t0 < p.wait_ns) {
+            while (!mbar_test_wait(&ms.drain, 0) && globaltimer() - t0 < kDrainNs) {
             }
         }
         __syncwarp();

@@ -375,6 +375,48 @@ def test_offsets_past_32_bits():
         t.check(*t.call(kernel))
 
 
+@pytest.mark.parametrize("T", [8, 24])  # one CTA per query tile, and pairs
+def test_a_wait_that_runs_out_is_reported_and_the_workspace_recovers(T):
+    # A limit of 1 us: the scores of the first tile (eight stages of keys at head_dim 512, out of DRAM as L2 holds
+    # something else) take some 4 us to come, so the kernel gives up by itself, reports it and returns.
+    t = Tree([T, T - 3], [6000, 7000], T=T, hq=16, hkv=2, d=512, seed=19)
+    torch.empty(256 << 20, dtype=torch.uint8, device="cuda").zero_()
+    t.call("tc", wait_limit_us=1)
+    ws = t.ws
+    assert t.error() & B.DEVERR_TIMEOUT
+    out, lse = t.call("tc", workspace=ws)
+    t.ws = ws
+    assert t.error() == 0
+    t.check(out, lse)
+
+
+def test_wrapper_refusals_on_the_gpu():
+    t = Tree([4, 4], [40, 50], d=64, seed=20)
+    dev = (torch.from_numpy(t.table).cuda(), torch.tensor(t.lens, dtype=torch.int32, device="cuda"),
+           torch.from_numpy(t.parents).cuda())
+    for bad in (dict(q=t.q.float()), dict(q=t.q[:, :, ::2]), dict(parents=dev[2].long()), dict(parents=dev[2][:1]),
+                dict(lens=dev[1].cpu()), dict(table=dev[0][:, ::2]), dict(out=torch.empty_like(t.q, dtype=torch.float32)),
+                dict(lse=torch.empty(3, device="cuda")), dict(num_nodes=torch.zeros(3, dtype=torch.int32, device="cuda")),
+                dict(v=t.v[:-1]), dict(workspace=torch.zeros(1 << 20, dtype=torch.uint8))):
+        a = dict(q=t.q, k=t.k, v=t.v, table=dev[0], lens=dev[1], parents=dev[2])
+        kw = {k: v for k, v in bad.items() if k not in a}
+        a.update({k: v for k, v in bad.items() if k in a})
+        with pytest.raises((ValueError, TypeError)):
+            dfl.tree_attn(a["q"], a["k"], a["v"], a["table"], a["lens"], a["parents"], **kw)
+    with pytest.raises(dfl.DflashError):
+        dfl.tree_attn(t.q, t.k, t.v, *dev, workspace=torch.zeros(512, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(dfl.DflashError):
+        dfl.tree_attn(t.q, t.k, t.v, *dev, out=t.q)
+    x = torch.zeros((2, 9), device="cuda")
+    for kw in (dict(top_k=10), dict(top_k=-1), dict(temperature=0.0), dict(temperature=float("nan"))):
+        with pytest.raises(dfl.DflashError):
+            dfl.token_logprobs(x, **kw)
+    with pytest.raises(ValueError):
+        dfl.token_logprobs(x, torch.zeros((2, 3), dtype=torch.int64, device="cuda"))
+    with pytest.raises(TypeError):
+        dfl.token_logprobs(x.half())
+
+
 # ------------------------------------------------------------------------- log probabilities
 
 

@@ -42,6 +42,14 @@ struct TreeAttnParams {
     unsigned long long wait_ns;
 };
 
+// The CUDA-core kernel's 64-dim chunks for head_dim D (1, 2, 4 or 8), and the CTAs of it that an SM holds with query
+// tiles of `rows`: its registers are bounded to that.
+constexpr int simt_chunks(int D) { return D <= 64 ? 1 : D <= 128 ? 2 : D <= 256 ? 4 : 8; }
+constexpr int simt_ctas_per_sm(int D, int rows)
+{
+    return rows <= 16 ? (D <= 128 ? 3 : 2) : rows <= 32 ? (D <= 128 ? 2 : 1) : (D <= 64 ? 2 : 1);
+}
+
 // The query tile shape and the number of ranges of a call, for the kernel `kernel` (DFLASH_KERNEL_SIMT or _TC).
 void tree_attn_plan(TreeAttnParams& p, int kernel);
 bool tree_tc_supports(const dflash_dims* d);

@@ -96,8 +96,8 @@ void tree_attn_plan(TreeAttnParams& p, int kernel)
     p.DV = !tc ? p.D : p.D <= 64 && !p.pair ? 64 : p.D <= 128 ? 128 : 256;
     p.ndv = (p.D + p.DV - 1) / p.DV;
     p.n_sub = (p.G / p.Gc) * p.nrt * p.ndv;
-    // one wave: the tensor-core kernel and the wide SIMT tiles hold one CTA per SM, the SIMT kernel at head_dim 64 two
-    const int32_t ctas = device_sm_count() * (!tc && p.D <= 64 ? 2 : 1);
+    // one wave: the tensor-core kernel holds one CTA per SM
+    const int32_t ctas = device_sm_count() * (tc ? 1 : simt_ctas_per_sm(64 * simt_chunks(p.D), p.rows));
     p.ranges = std::max(1, ctas / p.n_sub);
 }
 

@@ -4,12 +4,14 @@
 //   s_ij = scale <q_i, k_j> over the keys that node i sees, out_i = sum_j softmax(s_i)_j v_j
 //
 // A CTA of 256 threads owns a tile of up to 64 query rows (node x head) and streams its range's key
-// tiles of 64 keys once. Products are register-tiled: a thread holds 4 rows x 4 keys of the scores and 4 rows x
-// 4 dims of every 64-dim chunk of the output, so each value read from shared memory feeds four to
-// sixteen FMAs. K and V pass through two shared buffers of 64 keys x 64 dims (widened to fp32); the next
+// tiles of 64 keys once. Products are register-tiled: a thread holds R rows x 4 keys of the scores and R rows x
+// 4 dims of every 64-dim chunk of the output, so each value read from shared memory feeds R to 4 R FMAs; R is 4, or 2
+// or 1 where a KV head has no more than 32 or 16 rows (a single token's rows in tiles of 64 took 335 us for 4 requests
+// of 8192 keys, all but 6 % of the FMAs on dead rows). K and V pass through two shared buffers of 64 keys x 64 dims (widened to fp32); the next
 // chunk's global loads are in flight in registers while the current one is used, and one barrier per chunk is enough.
 // The softmax is online: running maximum and sum per row in fp32, replicated over the row's 16 threads.
-// Bound: the FMA pipe (2 D FMAs per row and key against 8 D bytes per key shared by 64 rows).
+// Bound: the FMA pipe for full tiles (2 D FMAs per row and key against 8 D bytes per key shared by 64 rows), the loads
+// in flight for few rows.
 #include <cmath>
 
 #include "tree_attn.cuh"
@@ -18,16 +20,15 @@ namespace dflash {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 64;
 constexpr int kKeys = 64;
 constexpr int kLd = 68;  // floats per shared row of 64: 16-byte loads of 8 rows fall on distinct banks
 
 struct SimtTreeSmem {
     static int q_ld(int D) { return (D + 63) / 64 * 64 + 4; }
-    static size_t bytes(int D)
+    static size_t bytes(int D, int rows)
     {
-        return sizeof(float) * ((size_t)kRows * q_ld(D) + 3 * kKeys * kLd) +
-               sizeof(int32_t) * (DFLASH_MAX_TREE_NODES + kRows + kRows * (DFLASH_MAX_TREE_NODES / 32));
+        return sizeof(float) * ((size_t)rows * (q_ld(D) + kLd) + 2 * kKeys * kLd) +
+               sizeof(int32_t) * (DFLASH_MAX_TREE_NODES + rows + rows * (DFLASH_MAX_TREE_NODES / 32));
     }
 };
 
@@ -63,9 +64,11 @@ __device__ __forceinline__ void fetch16(const TreeAttnParams& p, const void* bas
     }
 }
 
-template <int NC>  // 64-dim chunks
-__global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttnParams p)
+template <int NC, int R>  // 64-dim chunks, rows per thread
+__global__ void __launch_bounds__(kThreads, simt_ctas_per_sm(NC * 64, 16 * R))
+    tree_attn_simt_kernel(const TreeAttnParams p)
 {
+    constexpr int kRows = 16 * R;
     extern __shared__ float smem[];
     const int q_ld = NC * 64 + 4;
     float* Qs = smem;                      // [kRows][q_ld]
@@ -95,6 +98,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
             float v[16];
             const int32_t node = node0 + lr / p.Gc, head = g * p.G + st.gc * p.Gc + lr % p.Gc;
             fetch16(p, p.q, (((int64_t)b * p.T + node) * p.Hq + head) * p.D, lr < live, d, v);
+            if (lr >= kRows) continue;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 *reinterpret_cast<float4*>(Qs + lr * q_ld + d + 4 * u) =
@@ -104,15 +108,15 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
         tree_walk_nodes(p, w.req, node0, min(p.npt, n - node0), par_s, anc_s, lo_s, tid, kThreads);
         // (the first chunk's barrier below makes the walk's results visible before the first mask)
 
-        float o[NC][4][4], m[4], l[4];
+        float o[NC][R][4], m[R], l[R];
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) o[c][i][u] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
         }
@@ -143,9 +147,9 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
         };
         for (int32_t t = w.t0; t < w.t1; ++t) {
             const int32_t k0 = (w.req.tile0 + t) * kKeys;
-            float s[4][4];
+            float s[R][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 1
@@ -157,14 +161,14 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
                     fetch16(p, p.v, off, off >= 0, ld0, nxt);
 #pragma unroll 4
                 for (int d = 0; d < 64; d += 4) {
-                    float4 qv[4], kv[4];
+                    float4 qv[R], kv[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        qv[i] = *reinterpret_cast<const float4*>(Qs + (ty * 4 + i) * q_ld + c * 64 + d);
+                    for (int i = 0; i < R; ++i)
+                        qv[i] = *reinterpret_cast<const float4*>(Qs + (ty * R + i) * q_ld + c * 64 + d);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (tx + 16 * j) * kLd + d);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < R; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
@@ -175,10 +179,10 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
                 }
             }
             const bool edge = k0 + kKeys > ctx || (p.window > 0 && k0 < ctx + n - p.window + 1);
-            float alpha[4];
+            float alpha[R];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = ty * 4 + i;
+            for (int i = 0; i < R; ++i) {
+                const int row = ty * R + i;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -220,18 +224,18 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
                 else
                     fetch16(p, p.k, next_off, next_off >= 0, ld0, nxt);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) o[c][i][u] *= alpha[i];
 #pragma unroll 2
                 for (int k = 0; k < kKeys; k += 4) {
-                    float4 pv[4], vv[4];
+                    float4 pv[R], vv[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (ty * 4 + i) * kLd + k);
+                    for (int i = 0; i < R; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (ty * R + i) * kLd + k);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) vv[j] = *reinterpret_cast<const float4*>(vs + (k + j) * kLd + tx * 4);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < R; ++i) {
                         const float pr[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -248,8 +252,8 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
         const bool whole = w.whole();
         const int64_t prow = tree_part_row(p, range, sub, w.slot());
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = ty * 4 + i;
+        for (int i = 0; i < R; ++i) {
+            const int row = ty * R + i;
             if (row >= live) continue;
             const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
             const float lse = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
@@ -282,28 +286,32 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const TreeAttn
     }
 }
 
+template <int NC, int R>
+cudaError_t launch_nr(const TreeAttnParams& p, cudaStream_t stream)
+{
+    const size_t smem = SimtTreeSmem::bytes(NC * 64, 16 * R);
+    cudaError_t e =
+        cudaFuncSetAttribute(tree_attn_simt_kernel<NC, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    tree_attn_simt_kernel<NC, R><<<p.ranges * p.n_sub, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
 template <int NC>
 cudaError_t launch_nc(const TreeAttnParams& p, cudaStream_t stream)
 {
-    const size_t smem = SimtTreeSmem::bytes(NC * 64);
-    cudaError_t e =
-        cudaFuncSetAttribute(tree_attn_simt_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    tree_attn_simt_kernel<NC><<<p.ranges * p.n_sub, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return p.rows <= 16 ? launch_nr<NC, 1>(p, stream)
+                        : p.rows <= 32 ? launch_nr<NC, 2>(p, stream) : launch_nr<NC, 4>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_attn_simt(const TreeAttnParams& p, cudaStream_t stream)
 {
-    switch ((p.D + 63) / 64) {
+    switch (simt_chunks(p.D)) {
     case 1: return launch_nc<1>(p, stream);
     case 2: return launch_nc<2>(p, stream);
-    case 3: return launch_nc<3>(p, stream);
     case 4: return launch_nc<4>(p, stream);
-    case 5:
-    case 6: return launch_nc<6>(p, stream);
     default: return launch_nc<8>(p, stream);
     }
 }

@@ -541,8 +541,8 @@ DFLASH_API dflash_status dflash_tree_attn(const void* q, const void* k_cache, co
  *   accepted_len, next_token   device int32 [batch]; path device int32 [batch, max_nodes]; written.
  *   target_argmax device int32 [batch, max_nodes] or NULL.
  *   device_error  device uint32 word or NULL (DFLASH_DEVERR_TREE).
- *   workspace     device, 256-byte aligned, dflash_tree_accept_workspace_bytes() long, zeroed once before its first use;
- *                 the call leaves it zeroed. Layout: a fixed 512 KB block of row keys, then one of
+ *   workspace     device, 256-byte aligned, dflash_tree_accept_workspace_bytes() long, zeroed once before its
+ *                 first use; the call leaves it zeroed. Layout: a fixed 512 KB block of row keys, then one of
  *                 per-request counters, so one workspace serves calls of any size.
  * Limits: batch >= 1, 1 <= max_nodes <= DFLASH_MAX_TREE_NODES, batch * max_nodes <= 65535,
  * 1 <= vocab < 2^31. Invalid arguments are reported before any launch. Asynchronous on `stream`;

@@ -830,8 +830,8 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
         if lse is None and want_lse:
             lse = fresh(qs[:2], dtype=torch.float32, device=dev)
         st = lib.dflash_tree_attn(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, parents_at, nodes_at, dims_ref, T, window,
-            1.0 / math.sqrt(qs[2]) if scale is None else scale, out.data_ptr(),
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, parents_at, nodes_at,
+            dims_ref, T, window, 1.0 / math.sqrt(qs[2]) if scale is None else scale, out.data_ptr(),
             None if lse is None else lse.data_ptr(), KERNELS[kernel],
             None if workspace is None else workspace.data_ptr(), nbytes, wait_limit_us, handle)
     finally:
@@ -889,8 +889,8 @@ def tree_accept(logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tenso
         if workspace is None:
             workspace = _tree_workspace("tree_accept", dev, handle, nbytes, nbytes)
         st = lib.dflash_tree_accept(
-            logits.data_ptr(), code, B, T, V, row, tokens_at, parents_at, nodes_at, accepted.data_ptr(), path.data_ptr(), nxt.data_ptr(),
-            argmax.data_ptr() if want_argmax else None, word, workspace.data_ptr(), nbytes, handle)
+            logits.data_ptr(), code, B, T, V, row, tokens_at, parents_at, nodes_at, accepted.data_ptr(),
+            path.data_ptr(), nxt.data_ptr(), argmax.data_ptr() if want_argmax else None, word, workspace.data_ptr(), nbytes, handle)
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
@@ -944,7 +944,8 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.
             new_lens = torch.empty(batch, dtype=_I32, device=dev)
         st = lib.dflash_tree_commit(
             k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, path_at, accepted_at, nodes_at,
-            new_lens.data_ptr(), dims_ref, T, k_cache.shape[0] if first else 1, k_cache.stride(0) if first else 0, word, handle)
+            new_lens.data_ptr(), dims_ref, T, k_cache.shape[0] if first else 1, k_cache.stride(0) if first else 0,
+            word, handle)
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)

@@ -6,25 +6,25 @@
 // differences stay exact to fp32 whatever the size of the logits, and a row with one likely token keeps its
 // small entropy.
 //
-// A row is cut into slices, a CTA of 128 threads each, streamed in steps of 16 values a thread with the next step's
-// loads in flight; no barrier until its end. Beside the sums a thread keeps the maximum of each sixteenth of its
-// steps: of a group of values.
+// A row is cut into slices, a CTA of 128 threads each, streamed in steps of 16 values a thread with the next
+// step's loads in flight; no barrier until its end. Beside the sums a thread keeps the maximum of each
+// sixteenth of its steps: of a group of values.
 //
 // Selection. A value and its id form a 64-bit key (order-preserving image of the value above the id's
-// complement), all distinct, so "the k largest keys" is the definition. At the slice's end the threads' maxima give a
-// bound: sorted within each warp (shuffles), the least of the four warps' ceil(k / 4)-th largest has k values at or
-// above it. Only groups whose maximum reaches it are read again (some 70 to 100 of 2048 for k = 64, four percent of a
-// row of 152k), and only their values that reach it become candidates. Candidates and kept keys are ranked
-// against each other (a key's rank is the number of larger ones; no sort) and the first k stay. The buffer holds 256
-// candidates of each warp; a warp that might add more waits for a merge, so nothing but the time depends on the
-// data: a row of equal logits reads every group again.
-// A thread's values of a step are whole sectors, so that reading a group again fetches little beside it. Measured, k = 64
-// beside none: 1000 rows of 151937 fp32 137 and 107 us (floor 90), bf16 88 and 66 (45); 4000 rows of 32000 bf16 100
-// and 61 (38). (Candidates picked step by step, with a sort of 256 per merge, took 460 us for the first, with merges by
-// rank at every doubling of what has been seen 143; and 190 for the last: merges, not the stream, took the time.)
+// complement), all distinct, so "the k largest keys" is the definition. At the slice's end the threads' maxima
+// give a bound: sorted within each warp (shuffles), the least of the four warps' ceil(k / 4)-th largest has k
+// values at or above it. Only groups whose maximum reaches it are read again (some 70 to 100 of 2048 for k =
+// 64, four percent of a row of 152k), and only their values that reach it become candidates. Candidates and
+// kept keys are ranked against each other (a key's rank is the number of larger ones; no sort) and the first k
+// stay. The buffer holds 256 candidates of each warp; a warp that might add more waits for a merge, so nothing
+// but the time depends on the data: a row of equal logits reads every group again. A thread's values of a step
+// are whole sectors, so that reading a group again fetches little beside it. Measured, k = 64 beside none: 1000
+// rows of 151937 fp32 137 and 107 us (floor 90), bf16 88 and 66 (45); 4000 rows of 32000 bf16 100 and 61 (38).
+// (Candidates picked step by step, with a sort of 256 per merge, took 460 us for the first, with merges by rank
+// at every doubling of what has been seen 143; and 190 for the last: merges, not the stream, took the time.)
 //
-// Slices leave their sums and keys in the workspace; the last CTA of a row to arrive (a counter, no waiting) merges
-// them the same way and writes the row.
+// Slices leave their sums and keys in the workspace; the last CTA of a row to arrive (a counter, no waiting)
+// merges them the same way and writes the row.
 #include <algorithm>
 #include <cmath>
 

@@ -9,14 +9,14 @@ namespace dflash {
 // One dflash_tree_attn call, validated on the host.
 //
 // Work. A query tile is the rows of npt nodes x Gc heads of one KV head (row = node * Gc + head, `rows` of
-// them); a request has n_sub = (G / Gc) * nrt * ndv of them, nrt being the node tiles, per KV head, ndv being the slices of the
-// value's dims that one CTA's accumulators hold. Every one of them reads the same K/V, so the key tiles of
-// all (request, KV head) pairs, laid end to end, are cut into `ranges` equal ranges and a CTA
-// takes (range, query tile): each range is streamed by the n_sub CTAs of consecutive block
-// numbers at about the same time, out of L2 but for the first. A range may hold the end of one pair's
-// keys, whole pairs, and the start of another's: whatever the lengths, every CTA streams the same number of
-// key tiles to within one. A pair that lies in several ranges leaves one normalised
-// partial per range, and the join kernel merges them by their log-sum-exp.
+// them); a request has n_sub = (G / Gc) * nrt * ndv of them, nrt being the node tiles, per KV head, ndv being
+// the slices of the value's dims that one CTA's accumulators hold. Every one of them reads the same K/V, so the
+// key tiles of all (request, KV head) pairs, laid end to end, are cut into `ranges` equal ranges and a CTA
+// takes (range, query tile): each range is streamed by the n_sub CTAs of consecutive block numbers at about the
+// same time, out of L2 but for the first. A range may hold the end of one pair's keys, whole pairs, and the
+// start of another's: whatever the lengths, every CTA streams the same number of key tiles to within one. A
+// pair that lies in several ranges leaves one normalised partial per range, and the join kernel merges them by
+// their log-sum-exp.
 struct TreeAttnParams {
     const void* q;
     const void* k;

@@ -1,19 +1,19 @@
 // Longest accepted path of drafted trees: the target's token at every node (argmax of its row of logits, the
 // smallest id among equal maxima) and the walk from the root along the drafted tokens that agree.
 //
-// The argmax is one stream over the real nodes' rows; padding rows are not read. The rows of all requests, laid end to
-// end, are cut into equal parts, one CTA each, four CTAs an SM (one wave): a CTA streams its part, four to eight
-// 16-byte loads in flight per thread, and settles a row where it ends. (A CTA per 64 KB of a row spent a third of its life in its
-// first load's latency and in the arrival at its end: 53 us for 452 rows of 262144 bf16 logits.) A thread keeps
-// (maximum, first id) in increasing id order, then forms a 64-bit key, the order-preserving image of the value above
-// the complement of the id, so that the largest key is the largest logit of smallest id; -0 is taken as +0 first,
-// so equal values have equal images. CTAs merge a row's keys with a 64-bit atomicMax, whose result does
-// not depend on the order.
+// The argmax is one stream over the real nodes' rows; padding rows are not read. The rows of all requests, laid
+// end to end, are cut into equal parts, one CTA each, four CTAs an SM (one wave): a CTA streams its part, four
+// to eight 16-byte loads in flight per thread, and settles a row where it ends. (A CTA per 64 KB of a row spent
+// a third of its life in its first load's latency and in the arrival at its end: 53 us for 452 rows of 262144
+// bf16 logits.) A thread keeps (maximum, first id) in increasing id order, then forms a 64-bit key, the
+// order-preserving image of the value above the complement of the id, so that the largest key is the largest
+// logit of smallest id; -0 is taken as +0 first, so equal values have equal images. CTAs merge a row's keys
+// with a 64-bit atomicMax, whose result does not depend on the order.
 //
-// Each CTA adds what it has read of a request's logits to the request's counter; the one that completes it (no waiting)
-// reads its rows' keys. Every node whose token is its parent's target token offers itself to the parent with an
-// atomicMin in shared memory, so each node knows its first agreeing child, and one thread follows those links. The keys
-// and the counters are left at zero.
+// Each CTA adds what it has read of a request's logits to the request's counter; the one that completes it (no
+// waiting) reads its rows' keys. Every node whose token is its parent's target token offers itself to the
+// parent with an atomicMin in shared memory, so each node knows its first agreeing child, and one thread
+// follows those links. The keys and the counters are left at zero.
 #include <algorithm>
 
 #include "tree_attn.cuh"
@@ -67,7 +67,8 @@ struct Vec<float> {
     }
     static __device__ __forceinline__ float largest(const uint4& w)
     {
-        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
+                     fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
     static __device__ __forceinline__ float one(const float* r, int64_t i) { return r[i]; }
 };

@@ -151,7 +151,8 @@ dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v
     if (out == q) return report_error(DFLASH_ERR_INVALID_ARG, "out must not alias q");
     if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(num_nodes, 4) ||
         !aligned(lse, 4))
-        return report_error(DFLASH_ERR_INVALID_ARG, "page_table, seq_lens, parents, num_nodes and lse must be 4-byte aligned");
+        return report_error(DFLASH_ERR_INVALID_ARG,
+                            "page_table, seq_lens, parents, num_nodes and lse must be 4-byte aligned");
     if (window < 0) return report_error(DFLASH_ERR_INVALID_ARG, "window %d < 0", window);
     if (!std::isfinite(scale) || !(scale > 0.f))
         return report_error(DFLASH_ERR_INVALID_ARG, "scale must be finite and > 0");
@@ -192,7 +193,8 @@ dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v
 
 size_t dflash_logprobs_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t top_k)
 {
-    if (num_rows < 0 || num_rows > 65535 || vocab < 1 || top_k < 0 || top_k > DFLASH_MAX_TOP_K || top_k > vocab) return 0;
+    if (num_rows < 0 || num_rows > 65535 || vocab < 1) return 0;
+    if (top_k < 0 || top_k > DFLASH_MAX_TOP_K || top_k > vocab) return 0;
     return logprobs_layout(num_rows, logprobs_slices(std::max(1, num_rows), vocab), top_k).total;
 }
 
@@ -222,7 +224,8 @@ dflash_status dflash_token_logprobs(const void* logits, dflash_dtype dtype, int3
     if (!aligned(logits, dtype == DFLASH_BF16 ? 2 : 4) || !aligned(tokens, 4) || !aligned(token_logp, 4) ||
         !aligned(log_z, 4) || !aligned(entropy, 4) || !aligned(top_tokens, 4) || !aligned(top_logp, 4) ||
         !aligned(device_error, 4))
-        return report_error(DFLASH_ERR_INVALID_ARG, "misaligned pointer (logits to their element size, the rest 4 bytes)");
+        return report_error(DFLASH_ERR_INVALID_ARG,
+                            "misaligned pointer (logits to their element size, the rest 4 bytes)");
     LogprobsParams p{};
     p.slices = logprobs_slices(num_rows, vocab);
     const LogprobsLayout wl = logprobs_layout(num_rows, p.slices, top_k);
@@ -276,10 +279,12 @@ dflash_status dflash_tree_accept(const void* logits, dflash_dtype dtype, int32_t
     if (!aligned(logits, dtype == DFLASH_BF16 ? 2 : 4) || !aligned(tokens, 4) || !aligned(parents, 4) ||
         !aligned(num_nodes, 4) || !aligned(accepted_len, 4) || !aligned(path, 4) || !aligned(next_token, 4) ||
         !aligned(target_argmax, 4) || !aligned(device_error, 4))
-        return report_error(DFLASH_ERR_INVALID_ARG, "misaligned pointer (logits to their element size, the rest 4 bytes)");
+        return report_error(DFLASH_ERR_INVALID_ARG,
+                            "misaligned pointer (logits to their element size, the rest 4 bytes)");
     const size_t need = dflash_tree_accept_workspace_bytes();
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
-        return report_error(DFLASH_ERR_WORKSPACE, "tree acceptance needs a 256-byte aligned workspace of %zu bytes", need);
+        return report_error(DFLASH_ERR_WORKSPACE, "tree acceptance needs a 256-byte aligned workspace of %zu bytes",
+                            need);
     TreeAcceptParams p{};
     p.logits = logits;
     p.dtype = dtype;

@@ -170,7 +170,10 @@ struct PieceWalk {
             if (++g == p.Hkv) {
                 g = 0;
                 do {
-                    ++b;
+                    if (++b >= p.B) {  // not reached: the range lies below the total
+                        left = 0;
+                        return;
+                    }
                     req = tree_request(p, b);
                 } while (req.nt == 0);
             }
@@ -220,8 +223,8 @@ __device__ __forceinline__ int32_t tree_parent(const int32_t* parents, int32_t i
 // between them. par_s[T] takes the parents; then anc_s[i * words + w] takes the nodes that node0 + i sees
 // (bit j of word w is node 32 w + j) and lo_s[i] the first context key that it sees. A node walks
 // up to the root: as a parent comes before its children the walk ends, whatever the table holds.
-__device__ __forceinline__ void tree_load_parents(const TreeAttnParams& p, int32_t b, int32_t n, int32_t* par_s, int tid,
-                                                  int nthreads)
+__device__ __forceinline__ void tree_load_parents(const TreeAttnParams& p, int32_t b, int32_t n, int32_t* par_s,
+                                                  int tid, int nthreads)
 {
     for (int32_t i = tid; i < n; i += nthreads) par_s[i] = tree_parent(p.parents + (int64_t)b * p.T, i, p.err);
 }

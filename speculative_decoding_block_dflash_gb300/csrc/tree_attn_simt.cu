@@ -1,17 +1,17 @@
-// Tree attention on the CUDA cores: the fp32 path, and bf16 for layouts that the tensor-core kernel does
-// not take.
+// Tree attention on the CUDA cores: the fp32 path, and bf16 for layouts that the tensor-core kernel does not
+// take.
 //
 //   s_ij = scale <q_i, k_j> over the keys that node i sees, out_i = sum_j softmax(s_i)_j v_j
 //
-// A CTA of 256 threads owns a tile of up to 64 query rows (node x head) and streams its range's key
-// tiles of 64 keys once. Products are register-tiled: a thread holds R rows x 4 keys of the scores and R rows x
-// 4 dims of every 64-dim chunk of the output, so each value read from shared memory feeds R to 4 R FMAs; R is 4, or 2
-// or 1 where a KV head has no more than 32 or 16 rows (a single token's rows in tiles of 64 took 335 us for 4 requests
-// of 8192 keys, all but 6 % of the FMAs on dead rows). K and V pass through two shared buffers of 64 keys x 64 dims (widened to fp32); the next
-// chunk's global loads are in flight in registers while the current one is used, and one barrier per chunk is enough.
-// The softmax is online: running maximum and sum per row in fp32, replicated over the row's 16 threads.
-// Bound: the FMA pipe for full tiles (2 D FMAs per row and key against 8 D bytes per key shared by 64 rows), the loads
-// in flight for few rows.
+// A CTA of 256 threads owns a tile of up to 64 query rows (node x head) and streams its range's key tiles of 64
+// keys once. Products are register-tiled: a thread holds R rows x 4 keys of the scores and R rows x 4 dims of
+// every 64-dim chunk of the output, so each value read from shared memory feeds R to 4 R FMAs; R is 4, or 2 or
+// 1 where a KV head has no more than 32 or 16 rows (a single token's rows in tiles of 64 took 335 us for 4
+// requests of 8192 keys, all but 6 % of the FMAs on dead rows). K and V pass through two shared buffers of 64
+// keys x 64 dims (widened to fp32); the next chunk's global loads are in flight in registers while the current
+// one is used, and one barrier per chunk is enough. The softmax is online: running maximum and sum per row in
+// fp32, replicated over the row's 16 threads. Bound: the FMA pipe for full tiles (2 D FMAs per row and key
+// against 8 D bytes per key shared by 64 rows), the loads in flight for few rows.
 #include <cmath>
 
 #include "tree_attn.cuh"
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, simt_ctas_per_sm(NC * 64, 16 * R))
                         vis = row < live;
                         if (vis) {
                             const int32_t a = key - ctx;
-                            vis = a < 0 ? key >= lo_s[nd] : (key < L && ((anc_s[nd * words + (a >> 5)] >> (a & 31)) & 1u));
+                            vis = a < 0 ? key >= lo_s[nd]
+                                        : (key < L && ((anc_s[nd * words + (a >> 5)] >> (a & 31)) & 1u));
                         }
                     }
                     s[i][j] = vis ? s[i][j] * p.scale : -INFINITY;

@@ -4,43 +4,44 @@
 //   S [128 rows x 128 keys] = Q [128 x D] . K^T        (A: Q in shared memory, B: the K tile)
 //   O [128 rows x DV]      += P [128 x 128] . V        (A: P in TMEM, B: the V tile, MN-major)
 //
-// A query row is a (node, head of the KV head's group), a TMEM lane. Two softmax threads share a row's tile, 64 keys each:
-// they read their scores once into registers, exchange one maximum through shared memory, and hand over their half
-// of P. (A thread per row, alternate tiles to two warpgroups and O accumulators, took 1.45 us a
-// tile, two passes over TMEM, on the way between two MMAs: 158 us for the ragged batch of 64-node trees.) P (bf16) overwrites its own S, thus costs
-// neither shared memory nor TMEM, and shared memory is left to Q and the ring: what bounds the kernel is
-// the K/V stream, whose rate is the bytes in flight over the latency.
+// A query row is a (node, head of the KV head's group), a TMEM lane. Two softmax threads share a row's tile, 64
+// keys each: they read their scores once into registers, exchange one maximum through shared memory, and hand
+// over their half of P. (A thread per row, alternate tiles to two warpgroups and O accumulators, took 1.45 us a
+// tile, two passes over TMEM, on the way between two MMAs: 158 us for the ragged batch of 64-node trees.) P
+// (bf16) overwrites its own S, thus costs neither shared memory nor TMEM, and shared memory is left to Q and
+// the ring: what bounds the kernel is the K/V stream, whose rate is the bytes in flight over the latency.
 //
-// TMEM (512 columns): S0, S1 (128 each) and up to 256 of O; for head_dim above 256 a CTA computes 256 of the output's dims from
-// the whole S. A query tile is up to 128 rows; step t of a piece (one range's part of a request and KV head) is its key
-// tile t, with S buffer t % 2. The MMA warp does: S(0), S(1), then for every t: O += P(t) V, S(t + 2), which reuses the
-// buffer of P(t) (MMAs of one thread execute in order), so S(t + 1) waits for the softmax while S(t)'s P is multiplied.
+// TMEM (512 columns): S0, S1 (128 each) and up to 256 of O; for head_dim above 256 a CTA computes 256 of the
+// output's dims from the whole S. A query tile is up to 128 rows; step t of a piece (one range's part of a
+// request and KV head) is its key tile t, with S buffer t % 2. The MMA warp does: S(0), S(1), then for every t:
+// O += P(t) V, S(t + 2), which reuses the buffer of P(t) (MMAs of one thread execute in order), so S(t + 1)
+// waits for the softmax while S(t)'s P is multiplied.
 //
-// More than 128 rows per KV head: CTA pairs (clusters of two, cta_group::2). The two CTAs hold neighbouring query tiles and
-// share every MMA (M = 256): each loads half of the K tile's keys and half of the V tile's dims, so a K/V byte
-// enters one SM for 256 rows, and an SM reads half of each B operand from its shared memory, which is what bounds an
-// MMA of 128 x 128 x 16 (97 cycles measured with both operands in one SM's shared memory, against 64 at the tensor
-// peak). The even CTA's thread issues; its commits arrive in both CTAs; softmax warps of both arrive at the even
-// CTA's barriers. (Two tiles of 128 rows in one CTA instead took 177 us for the ragged batch of 64-node trees, 2.6 us
-// a tile of 128 keys, of which the MMAs were 1.5.)
+// More than 128 rows per KV head: CTA pairs (clusters of two, cta_group::2). The two CTAs hold neighbouring
+// query tiles and share every MMA (M = 256): each loads half of the K tile's keys and half of the V tile's
+// dims, so a K/V byte enters one SM for 256 rows, and an SM reads half of each B operand from its shared
+// memory, which is what bounds an MMA of 128 x 128 x 16 (97 cycles measured with both operands in one SM's
+// shared memory, against 64 at the tensor peak). The even CTA's thread issues; its commits arrive in both CTAs;
+// softmax warps of both arrive at the even CTA's barriers. (Two tiles of 128 rows in one CTA instead took 177
+// us for the ragged batch of 64-node trees, 2.6 us a tile of 128 keys, of which the MMAs were 1.5.)
 //
-// Online softmax about a lazy maximum: a row's maximum moves only when a score exceeds it by 2^8 in the exp2 domain; O
-// and the sum are then rescaled in place. P <= 2^8 in bf16 rounds each probability to 2^-8 relative, the same choice the
-// block attention makes: the products with V average such errors out, and P in fp32 would need tf32
-// MMAs of a quarter of the rate. The row sums add the unrounded probabilities in fp32.
+// Online softmax about a lazy maximum: a row's maximum moves only when a score exceeds it by 2^8 in the exp2
+// domain; O and the sum are then rescaled in place. P <= 2^8 in bf16 rounds each probability to 2^-8 relative,
+// the same choice the block attention makes: the products with V average such errors out, and P in fp32 would
+// need tf32 MMAs of a quarter of the rate. The row sums add the unrounded probabilities in fp32.
 //
-// Masks are only looked at in tiles that hold tree keys or a window's edge: a node's visible keys of 32 positions are
-// one word, made from its ancestors' bits. V rows that no node sees are zeroed in shared memory, as 0 x NaN would
-// reach every row.
+// Masks are only looked at in tiles that hold tree keys or a window's edge: a node's visible keys of 32
+// positions are one word, made from its ancestors' bits. V rows that no node sees are zeroed in shared memory,
+// as 0 x NaN would reach every row.
 //
-// Warps: 0-7 softmax and output, 8-10 TMA producers, 11 the MMA issuer. Ring stages are 16 KB: K 128 keys
-// x 64 dims, V 64 keys x 128 dims (128 keys x 64 dims at DV = 64); in a pair each CTA's halves are K 64 keys x
-// 128 dims, V 64 keys x 128 dims (DV = 256) or 128 keys x 64 dims. A box is 64 dims of up to 64 tokens of one page; its
-// id is read one stage ahead by the lane that issues it. Boxes past the keys or before the window are
+// Warps: 0-7 softmax and output, 8-10 TMA producers, 11 the MMA issuer. Ring stages are 16 KB: K 128 keys x 64
+// dims, V 64 keys x 128 dims (128 keys x 64 dims at DV = 64); in a pair each CTA's halves are K 64 keys x 128
+// dims, V 64 keys x 128 dims (DV = 256) or 128 keys x 64 dims. A box is 64 dims of up to 64 tokens of one page;
+// its id is read one stage ahead by the lane that issues it. Boxes past the keys or before the window are
 // fetched at an out-of-bounds page, which the TMA unit fills with zeros without a look at the table.
 //
-// Every mbarrier wait is bounded (p.wait_ns): on expiry the kernel records DFLASH_DEVERR_TIMEOUT, waits (bounded) for its
-// own copies and MMAs, frees TMEM and returns.
+// Every mbarrier wait is bounded (p.wait_ns): on expiry the kernel records DFLASH_DEVERR_TIMEOUT, waits
+// (bounded) for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
 
 #include <algorithm>
@@ -64,8 +65,8 @@ constexpr int kStageBytes = 16384;
 constexpr int kMaxStages = 13;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kOCol = 256;  // first TMEM column of O
-// After a failed wait, whatever the caller's limit: the bound of the waits for copies and MMAs in flight, and the time given
-// to copies that this CTA cannot wait for.
+// After a failed wait, whatever the caller's limit: the bound of the waits for copies and MMAs in flight, and
+// the time given to copies that this CTA cannot wait for.
 constexpr unsigned long long kDrainNs = 100000000ull;
 constexpr unsigned long long kCopyGraceNs = 1000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -145,7 +146,8 @@ __device__ __forceinline__ void store_f8(float* dst, const float* v)
 }
 
 // D (TMEM) (+)= A (TMEM, bf16 pairs) . B (shared memory)
-__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum)
+__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accum)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -155,7 +157,8 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-__device__ __forceinline__ void tc_mma2_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum)
+__device__ __forceinline__ void tc_mma2_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accum)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"

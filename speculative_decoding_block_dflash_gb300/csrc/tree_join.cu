@@ -29,7 +29,8 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
     const SubTile st = sub_tile(p, sub);
     const TreeReq rq = tree_request(p, b);
     const int32_t node0 = st.rt * p.npt;
-    if (rq.bad && g == 0 && sub == 0 && blockIdx.z == 0 && threadIdx.x == 0) raise_error(p.err, tree_request_error(p, rq));
+    if (rq.bad && g == 0 && sub == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+        raise_error(p.err, tree_request_error(p, rq));
     const int32_t n_here = rq.bad ? p.T : rq.n;
     const int32_t live = min(p.npt, n_here - node0) * p.Gc;
     int32_t r0 = 0, parts = 0;
@@ -63,7 +64,8 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
             for (int u = 0; u < V; u += kRun) {
                 const bool on = live_part && dim_of(u) < d_here;
                 if (V < 4) {
-                    const float2 y = on ? __ldcg(reinterpret_cast<const float2*>(src + dim_of(u))) : make_float2(0.f, 0.f);
+                    const float2 y = on ? __ldcg(reinterpret_cast<const float2*>(src + dim_of(u)))
+                                        : make_float2(0.f, 0.f);
                     x[u] = y.x;
                     x[u + 1] = y.y;
                 } else {
@@ -130,7 +132,8 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
                 *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + o) =
                     __floats2bfloat162_rn(acc[u] * inv, acc[u + 1] * inv);
             else
-                *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) = make_float2(acc[u] * inv, acc[u + 1] * inv);
+                *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) =
+                    make_float2(acc[u] * inv, acc[u + 1] * inv);
         }
         if (lane == 0 && st.dv == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : m + logf(t);
     }

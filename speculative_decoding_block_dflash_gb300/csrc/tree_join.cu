@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
         parts = sh_parts;
     }
     cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();  // the next layer's attention may set itself up; it waits for this grid
     if (live <= 0 || parts == 1 || (parts == 0 && !rq.bad)) return;
     const int32_t d_here = min(p.DV, p.D - st.dv * p.DV);
     // A lane's floats: runs of four (two, of 64 dims), 128 dims apart, so that a warp's loads are whole lines.

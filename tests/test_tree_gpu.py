@@ -360,6 +360,66 @@ def test_same_bits_twice_on_streams_and_in_graphs(kernel, dtype):
             torch.testing.assert_close(w, g, rtol=0, atol=0, equal_nan=True)
 
 
+@pytest.mark.parametrize("kernel", ["tc", "simt"])
+def test_inputs_made_just_before(kernel):
+    # the attention may set itself up while the work before it still runs: copies, fills and kernels of its own and of
+    # another stream that write its inputs, eagerly and captured; and layers back to back that feed each other
+    t = Tree([12, 5, 1], [700, 90, 33], hq=16, hkv=4, d=128, page=16, seed=43)
+    dev = (torch.from_numpy(t.table).cuda(), torch.tensor(t.lens, dtype=torch.int32, device="cuda"),
+           torch.from_numpy(t.parents).cuda(), torch.tensor(t.nodes, dtype=torch.int32, device="cuda"))
+
+    def go(q, k, v, args):
+        return dfl.tree_attn(q, k, v, args[0], args[1], args[2], num_nodes=args[3], kernel=kernel)
+
+    ref = go(t.q, t.k, t.v, dev)[0]
+    second = go(ref, t.k, t.v, dev)[0]
+    torch.cuda.synchronize()
+    q, k, v = (torch.zeros_like(x) for x in (t.q, t.k, t.v))
+    args = [torch.zeros_like(x) for x in dev]
+    big = torch.zeros(64 << 20, device="cuda")
+    side = torch.cuda.Stream()
+
+    def work():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            big.add_(1.0)  # a few hundred microseconds before the inputs are there
+            v.copy_(t.v)
+            k.zero_()
+            k.add_(t.k)
+        big.mul_(0.5)
+        for x, y in zip(args, dev):
+            x.copy_(y)
+        q.copy_(t.q)
+        here.wait_stream(side)
+        first = go(q, k, v, args)[0]
+        return first, go(first, k, v, args)[0]
+
+    def wipe():
+        for x in [q, k, v] + args:
+            x.zero_()
+        torch.cuda.synchronize()
+
+    for _ in range(3):
+        wipe()
+        got = work()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], ref) and torch.equal(got[1], second)
+    wipe()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = work()
+    for _ in range(3):
+        wipe()
+        for x in got:
+            x.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        g.replay()  # nothing waits between the two
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], ref) and torch.equal(got[1], second)
+
+
 def test_offsets_past_32_bits():
     # a pool of more than 2^31 elements, its pages used from the end
     page, hkv, d = 64, 8, 128

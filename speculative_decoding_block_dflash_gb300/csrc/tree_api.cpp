@@ -328,6 +328,7 @@ dflash_status dflash_tree_commit(void* k_cache, void* v_cache, const int32_t* pa
         !aligned(path, 4) || !aligned(accepted_len, 4) || !aligned(num_nodes, 4) || !aligned(new_lens, 4) ||
         !aligned(device_error, 4))
         return report_error(DFLASH_ERR_INVALID_ARG, "misaligned pointer (caches 16 bytes, the rest 4)");
+    if (k_cache == v_cache) return report_error(DFLASH_ERR_INVALID_ARG, "k_cache and v_cache must not be one cache");
     const char* nl = reinterpret_cast<const char*>(new_lens);
     const size_t lens_bytes = sizeof(int32_t) * (size_t)dims->batch;
     auto overlaps = [&](const void* a, size_t bytes) {

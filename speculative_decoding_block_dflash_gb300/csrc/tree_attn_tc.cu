@@ -819,12 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float o[16];
 #pragma unroll
                     for (int u = 0; u < 16; ++u) o[u] = u2f(r[u]) * inv;
-                    if (!live_row) continue;
-                    if (!whole) {
+                    if (live_row && !whole) {
                         float* dst = p.part_out + prow * DV + c;
                         store_f8(dst, o);
                         store_f8(dst + 8, o + 8);
-                    } else {
+                    } else if (live_row) {
                         uint32_t pk[8];
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
@@ -836,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                         dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                     }
+                    __syncwarp();  // the next load takes the whole warp
                 }
             }
             tc_fence_before();

@@ -148,7 +148,7 @@ def test_tree_accept_refuses(lib, kw, code):
 
 
 def commit(lib, d=None, T=4, layers=2, layer_stride=1 << 20, **ptrs):
-    p = dict(k=FAKE, v=FAKE, table=FAKE, lens=8 * FAKE, path=FAKE, acc=FAKE, nodes=None, new=16 * FAKE, err=None)
+    p = dict(k=FAKE, v=32 * FAKE, table=FAKE, lens=8 * FAKE, path=FAKE, acc=FAKE, nodes=None, new=16 * FAKE, err=None)
     p.update(ptrs)
     d = dims() if d is None else d
     return lib.dflash_tree_commit(p["k"], p["v"], p["table"], p["lens"], p["path"], p["acc"], p["nodes"], p["new"],
@@ -164,6 +164,7 @@ def commit(lib, d=None, T=4, layers=2, layer_stride=1 << 20, **ptrs):
     (dict(k=None), B.ERR_INVALID_ARG), (dict(v=None), B.ERR_INVALID_ARG), (dict(table=None), B.ERR_INVALID_ARG),
     (dict(lens=None), B.ERR_INVALID_ARG), (dict(path=None), B.ERR_INVALID_ARG), (dict(acc=None), B.ERR_INVALID_ARG),
     (dict(k=FAKE + 8), B.ERR_INVALID_ARG), (dict(path=FAKE + 2), B.ERR_INVALID_ARG),
+    (dict(v=FAKE), B.ERR_INVALID_ARG),  # one cache for both
     # new_lens may be seq_lens itself, but overlap no other input, nor seq_lens in part
     (dict(new=8 * FAKE + 4), B.ERR_INVALID_ARG), (dict(new=FAKE), B.ERR_INVALID_ARG),
     (dict(new=16 * FAKE, nodes=16 * FAKE + 4), B.ERR_INVALID_ARG),

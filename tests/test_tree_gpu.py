@@ -622,6 +622,77 @@ def test_logprobs_many_rows_match_torch():
     assert ((ent + (want.exp() * want).sum(1)).abs() <= 32 * tol).all()
 
 
+def test_logprobs_repeats_streams_and_graphs():
+    # several slices a row, other sizes in between, and graphs whose workspaces are their own
+    g = torch.Generator(device="cuda").manual_seed(51)
+    cases = [(torch.randn((3, 90001), generator=g, device="cuda"), 20), (torch.randn((40, 7000), generator=g,
+             device="cuda").bfloat16(), 64)]
+    want = [dfl.token_logprobs(x, top_k=k) for x, k in cases]
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [dfl.token_logprobs(x, top_k=k, stream=st) for (x, k), st in zip(cases, s)]
+        again = [dfl.token_logprobs(x, top_k=k, stream=s[0]) for x, k in cases]
+        torch.cuda.synchronize()
+        for w, o, u in zip(want, got, again):
+            assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(w[1:], o[1:], u[1:]))
+    graphs, outs = [], []
+    for x, k in cases:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(dfl.token_logprobs(x, top_k=k))
+        graphs.append(gr)
+    for _ in range(4):
+        for o in outs:
+            for x in o[1:]:
+                x.fill_(-9)
+        torch.cuda.synchronize()
+        for gr, st in zip(graphs, s):
+            with torch.cuda.stream(st):
+                gr.replay()
+                gr.replay()
+        torch.cuda.synchronize()
+        for w, o in zip(want, outs):
+            assert all(torch.equal(a, b) for a, b in zip(w[1:], o[1:]))
+
+
+def test_largest_counts_of_rows_and_requests():
+    g = torch.Generator(device="cuda").manual_seed(52)
+    n = 65535
+    x = torch.randn((n, 7), generator=g, device="cuda")
+    _, ent, z, top, lp = dfl.token_logprobs(x, top_k=7)
+    want = torch.log_softmax(x.double(), 1)
+    sv, si = want.sort(dim=1, descending=True, stable=True)
+    assert (top == si).all() and ((lp - sv).abs() <= 2.0 ** -18).all()
+    # one-node trees and the largest trees
+    for nb, T in ((n, 1), (255, 256)):
+        logits = torch.randn((nb, T, 7), generator=g, device="cuda")
+        parents = torch.arange(-1, T - 1, dtype=torch.int32, device="cuda").repeat(nb, 1)
+        best = logits.argmax(2).int()
+        tokens = torch.roll(best, 1, 1)  # every node continues its parent as the target does
+        acc, path, nxt, arg = dfl.tree_accept(logits, tokens, parents)
+        assert torch.equal(arg, best) and (acc == T - 1).all() and torch.equal(nxt, best[:, -1])
+        assert torch.equal(path, torch.arange(T, dtype=torch.int32, device="cuda").repeat(nb, 1))
+    # a batch of the largest size: request b attends to its own key and the page all of them share
+    k = torch.zeros((2, 8, 1, 16), device="cuda")
+    v = torch.randn((2, 8, 1, 16), generator=g, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        kd, vd = k.to(dtype), v.to(dtype)
+        q = torch.randn((n, 1, 16), generator=g, device="cuda").to(dtype)
+        lens = torch.randint(1, 17, (n,), generator=g, device="cuda", dtype=torch.int32)
+        table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").repeat(n, 1)
+        root = torch.full((n, 1), -1, dtype=torch.int32, device="cuda")
+        out, lse = dfl.tree_attn(q, kd, vd, table, lens, root)
+        # zero scores: the mean of the values, lse = log(count); P and the products are exact, the mean is rounded once
+        mean = vd.double().view(16, 16).cumsum(0)[lens.long() - 1] / lens.double()[:, None]
+        eps = torch.finfo(dtype).eps
+        spread = vd.double().abs().view(16, 16).cumsum(0)[lens.long() - 1] / lens.double()[:, None]
+        # fp32 sums of up to 16 values: 17 roundings of half a step of 2^-23, beside the output's own
+        assert ((out[:, 0].double() - mean).abs() <= eps / 2 * mean.abs() + 17 * 2.0 ** -24 * spread).all()
+        # the logarithm of at most 16 and its scaling to base e: a few roundings of values below 4
+        assert ((lse[:, 0].double() - lens.double().log()).abs() <= 2.0 ** -19).all()
+
+
 # ------------------------------------------------------------------------------- acceptance
 
 
@@ -904,3 +975,67 @@ def test_a_serving_step_from_candidates_to_the_committed_cache():
     assert v.abs().max() < 5.5
     torch.testing.assert_close(l1, l2, rtol=1e-5, atol=1.01 * U16)
     torch.testing.assert_close(o1.float(), o2.float(), rtol=4 * U16, atol=2 * 5.5 * U16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_captured_step_serves_other_lengths_and_trees(dtype):
+    """One graph of all four calls, replayed for lengths, trees and logits that it was not captured with."""
+    g = torch.Generator(device="cuda").manual_seed(53)
+    rng = np.random.default_rng(53)
+    nb, T, V, page, hkv, hq, d, layers = 4, 21, 3001, 16, 2, 8, 64, 3
+    k = torch.zeros((layers, 80, page, hkv, d), dtype=dtype, device="cuda")
+    v, q = torch.zeros_like(k), torch.zeros((nb * T, hq, d), dtype=dtype, device="cuda")
+    logits = torch.zeros((nb, T, V), dtype=dtype, device="cuda")
+    tokens, parents = (torch.zeros((nb, T), dtype=torch.int32, device="cuda") for _ in range(2))
+    lens, nodes = (torch.full((nb,), n, dtype=torch.int32, device="cuda") for n in (T, T))
+    table = torch.randperm(80, generator=g, device="cuda").int().view(nb, 20)
+
+    def step():
+        scored = dfl.token_logprobs(logits, tokens.view(nb, T, 1), top_k=5)
+        outs = [dfl.tree_attn(q, k[i], v[i], table, lens, parents, num_nodes=nodes, window=w)
+                for i, w in ((0, 0), (1, 40), (2, 0))]
+        acc, path, nxt, best = dfl.tree_accept(logits, tokens, parents, num_nodes=nodes)
+        new = dfl.tree_commit(k, v, table, lens, path, acc, num_nodes=nodes, new_lens=lens)
+        assert new is lens
+        return list(scored) + [x for o in outs for x in o] + [acc, path, nxt, best]
+
+    graph = torch.cuda.CUDAGraph()
+    parents.fill_(-1)
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(4):
+        n = rng.integers(0, T + 1, nb)
+        ctx = rng.integers(0, 20 * page - T, nb)
+        table_n = np.array([[rng.integers(-1, max(1, i)) if i else -1 for i in range(T)] for _ in range(nb)], np.int32)
+        lens0 = torch.tensor(np.where(n > 0, ctx + n, ctx), dtype=torch.int32, device="cuda")
+        nodes.copy_(torch.tensor(n, dtype=torch.int32))
+        parents.copy_(torch.from_numpy(np.minimum(table_n, np.arange(T) - 1)))
+        for x in (q, logits, k, v):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        best = logits.float().argmax(2).int()
+        up = parents.long().clamp(min=0)
+        agree = torch.rand((nb, T), generator=g, device="cuda") < 0.7
+        tokens.copy_(torch.where(agree, best.gather(1, up), (best.gather(1, up) + 1) % V))
+        start = k.clone(), v.clone()
+        for x in got:
+            x.zero_()
+        lens.copy_(lens0)
+        graph.replay()
+        torch.cuda.synchronize()
+        from_graph = [x.clone() for x in got] + [lens.clone(), k.clone(), v.clone()]
+        k.copy_(start[0])
+        v.copy_(start[1])
+        lens.copy_(lens0)
+        eager = step()
+        torch.cuda.synchronize()
+        assert dfl.tree_attn_error() == 0
+        for a, b in zip(from_graph, list(eager) + [lens, k, v]):
+            assert torch.equal(a, b)
+        want = ot.tree_accept(logits.double().cpu().numpy(), tokens.cpu().numpy(), parents.cpu().numpy(), n)
+        for a, b in zip(eager[-4:], want):
+            np.testing.assert_array_equal(a.cpu().numpy(), b)
+        for cache, old in ((k, start[0]), (v, start[1])):
+            moved, new = ot.tree_commit(old.double().cpu().numpy(), table.cpu().numpy(), lens0.cpu().numpy(), want[1],
+                                        want[0], n)
+            assert (cache.double().cpu().numpy() == moved).all()
+        np.testing.assert_array_equal(lens.cpu().numpy(), new)

@@ -6,22 +6,23 @@
 // differences stay exact to fp32 whatever the size of the logits, and a row with one likely token keeps its
 // small entropy.
 //
-// A row is cut into slices, a CTA of 128 threads each, streamed in steps of 16 values a thread with the next
-// step's loads in flight; no barrier until its end. Beside the sums a thread keeps the maximum of each
-// sixteenth of its steps: of a group of values.
+// A row is cut into equal slices, a CTA of 128 threads each, streamed in steps of 16 values a thread with the
+// next step's loads in flight; no barrier until its end. Beside the sums a thread keeps the maximum of each
+// thirty-second of its steps: of a group of values.
 //
 // Selection. A value and its id form a 64-bit key (order-preserving image of the value above the id's
 // complement), all distinct, so "the k largest keys" is the definition. At the slice's end the threads' maxima
-// give a bound: sorted within each warp (shuffles), the least of the four warps' ceil(k / 4)-th largest has k
-// values at or above it. Only groups whose maximum reaches it are read again (some 70 to 100 of 2048 for k =
-// 64, four percent of a row of 152k), and only their values that reach it become candidates. Candidates and
-// kept keys are ranked against each other (a key's rank is the number of larger ones; no sort) and the first k
-// stay. The buffer holds 256 candidates of each warp; a warp that might add more waits for a merge, so nothing
-// but the time depends on the data: a row of equal logits reads every group again. A thread's values of a step
-// are whole sectors, so that reading a group again fetches little beside it. Measured, k = 64 beside none: 1000
-// rows of 151937 fp32 137 and 107 us (floor 90), bf16 88 and 66 (45); 4000 rows of 32000 bf16 100 and 61 (38).
-// (Candidates picked step by step, with a sort of 256 per merge, took 460 us for the first, with merges by rank
-// at every doubling of what has been seen 143; and 190 for the last: merges, not the stream, took the time.)
+// give a bound that k values or more reach. Only groups whose maximum reaches it are read again (some 70 to 100
+// of 4096 for k = 64), and only their values that reach it become candidates. Candidates and kept keys are
+// ranked against each other (a key's rank is the number of larger ones; no sort) and the first k stay. The
+// buffer holds 256 candidates of each warp; a warp that might add more waits for a merge, so nothing but the
+// time depends on the data: a row of equal logits reads every group again. A thread's values of a step are
+// whole sectors, so that reading a group again fetches little beside it. Measured, k = 64 beside none: 1000
+// rows of 151937 fp32 129 and 107 us (floor 90), bf16 82 and 67 (45); 4000 rows of 32000 bf16 100 and 61 (38);
+// 8 rows of 151936 bf16 27 and 10. (Candidates picked step by step, with a sort of 256 per merge, took 460 us
+// for the first, with merges by rank at every doubling of what has been seen 143, with 16 groups a thread in
+// place of 32 137. A bound from all four warps alone, and a short last slice, took 43 us for the 8 rows: a warp
+// without values left no bound.)
 //
 // Slices leave their sums and keys in the workspace; the last CTA of a row to arrive (a counter, no waiting)
 // merges them the same way and writes the row.
@@ -100,23 +101,26 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
-constexpr int kPhases = 16;  // groups per thread
+constexpr int kPhases = 32;  // groups per thread, a bit each
+constexpr int kList = kPhases / 2 * kThreads;
 
 // (17 KB a CTA: with 25 KB, eight to an SM, the loads in flight had too little of the L1 left: 104 -> 133 us without
 // top tokens.)
 struct Shared {
     Key kept[kMaxK];  // the k largest so far, largest first
     union {
-        float group[kPhases][kThreads];  // maxima, until the groups to read again are listed
-        Key cand[kCand];                 // then the waiting candidates
+        __nv_bfloat16 group[kPhases][kThreads];  // maxima rounded up, until it is known which groups to read again
+        Key cand[kCand];                         // then the waiting candidates
     };
-    uint16_t list[kPhases * kThreads];  // groups to read again: phase * kThreads + thread
-    int32_t n_list;
-    Key warp_key[kThreads / 32];
+    uint16_t list[kList];  // groups to read again: phase * kThreads + thread
+    int32_t warp_n[kThreads / 32];
     Key bound;                // keys at or below it are out
     int32_t n_kept, n_cand;
     int32_t last;
-    float warp_top[kThreads / 32];
+    union {
+        float warp_top[4][kThreads / 32];
+        Key warp_key[4][kThreads / 32];
+    };
     float red[3][kThreads / 32];
 };
 
@@ -163,10 +167,13 @@ __device__ __forceinline__ void merge(Shared& sh, int32_t k, int tid)
     __syncthreads();
 }
 
-// The j-th largest (from 0) of a warp's values.
+// A bound from one value of each thread: at least k of them reach it, or it is `none`, the least there is. For each
+// number of warps j the ceil(k / j)-th largest of a warp's, and of these the j-th largest: j warps hold k values from
+// there on. The best of the four is taken, so that warps without values (of a short slice) cost little.
 template <typename T>
-__device__ __forceinline__ T warp_nth(T x, int j, int lane)
+__device__ __forceinline__ T bound_of(T (&part)[4][kThreads / 32], int32_t k, int tid, T x, T none)
 {
+    const int lane = tid & 31;
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1) {
         const bool down = (lane & size) == 0;
@@ -177,21 +184,25 @@ __device__ __forceinline__ T warp_nth(T x, int j, int lane)
             x = larger ? (x > other ? x : other) : (x > other ? other : x);
         }
     }
-    return __shfl_sync(0xffffffffu, x, j);
-}
-
-// A bound from one key of each thread's (0: none), its largest: at least k keys exceed it, or it is the old one.
-__device__ __forceinline__ void raise_bound(Shared& sh, int32_t k, int tid, Key top)
-{
-    const Key nth = warp_nth(top, (k + kThreads / 32 - 1) / (kThreads / 32) - 1, tid & 31);
-    if ((tid & 31) == 0) sh.warp_key[tid >> 5] = nth;
+#pragma unroll
+    for (int j = 1; j <= 4; ++j)
+        if (lane == (k + j - 1) / j - 1) part[j - 1][tid >> 5] = x;
     __syncthreads();
-    if (tid == 0) {
-        Key least = sh.warp_key[0];
-        for (int w = 1; w < kThreads / 32; ++w) least = min(least, sh.warp_key[w]);
-        if (least > 0) sh.bound = max(sh.bound, least - 1);  // the key itself stays in
+    T best = none;
+#pragma unroll
+    for (int j = 1; j <= 4; ++j) {
+        if ((k + j - 1) / j > 32) continue;
+        // the j-th largest of four
+        const T a = part[j - 1][0], b = part[j - 1][1], c = part[j - 1][2], d = part[j - 1][3];
+        const T ab = a > b ? a : b, ba = a > b ? b : a, cd = c > d ? c : d, dc = c > d ? d : c;
+        const T low = ab > cd ? cd : ab, high = ba > dc ? ba : dc;  // the two between the largest and the least
+        const T nth = j == 1   ? (ab > cd ? ab : cd)
+                      : j == 2 ? (low > high ? low : high)
+                      : j == 3 ? (low > high ? high : low)
+                               : (ba > dc ? dc : ba);
+        best = nth > best ? nth : best;
     }
-    __syncthreads();
+    return best;
 }
 
 __device__ __forceinline__ void put(Shared& sh, Key key) { sh.cand[atomicAdd(&sh.n_cand, 1)] = key; }
@@ -225,87 +236,121 @@ __device__ __noinline__ void select_again(Shared& sh, int32_t k, const Slice sl,
     constexpr int kSecs = kVecs / 2;
     const int tid = threadIdx.x;
     // the bound: a value that k values or more reach (-inf where there are not that many)
-    const float nth = warp_nth(top, (k + kThreads / 32 - 1) / (kThreads / 32) - 1, tid & 31);
-    if ((tid & 31) == 0) sh.warp_top[tid >> 5] = nth;
-    __syncthreads();
-    float limit = sh.warp_top[0];
-#pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) limit = fminf(limit, sh.warp_top[i]);
+    float limit = bound_of(sh.warp_top, k, tid, top, -INFINITY);
+    uint32_t mine = 0;  // this thread's groups to read again
+#pragma unroll 4
     for (int32_t phase = 0; phase * sl.phase_len < sl.steps; ++phase)
-        if (sh.group[phase][tid] >= limit) sh.list[atomicAdd(&sh.n_list, 1)] = (uint16_t)(phase * kThreads + tid);
-    __syncthreads();  // the groups' maxima make room for candidates
+        if (__bfloat162float(sh.group[phase][tid]) >= limit) mine |= 1u << phase;
+    // where a thread's groups stand in the list, and how many there are of all threads
+    int32_t place = 0, n_list = 0;
+    auto count = [&](uint32_t groups) {
+        const int32_t n = __popc(groups);
+        int32_t incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, incl, off);
+            if ((tid & 31) >= off) incl += v;
+        }
+        if ((tid & 31) == 31) sh.warp_n[tid >> 5] = incl;
+        __syncthreads();  // (the first time also: the groups' maxima make room for candidates)
+        place = incl - n;
+        n_list = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < tid >> 5) place += sh.warp_n[i];
+            n_list += sh.warp_n[i];
+        }
+    };
+    count(mine);
+    uint32_t rest = 0;
+    const bool halves = n_list > kList;  // many equal values: half of the groups a time
+    if (halves) {
+        rest = mine & ~0xFFFFu;
+        mine &= 0xFFFFu;
+        __syncthreads();
+        count(mine);
+    }
     if (has_edge && edge_x >= limit) put(sh, make_key(edge_x, (uint32_t)edge_id));
     // the groups' 16-byte vectors, a group's `per` one after another, dealt to the threads four at a time
     const int32_t per = sl.phase_len * kVecs;
-    const int64_t total = (int64_t)sh.n_list * per;
     Key bound = 0;
-    int64_t from = 0;
 #pragma unroll 1
-    do {
-        uint4 v[kAgain];
-        int32_t at[kAgain];  // 16-byte vector of the slice, or -1
-#pragma unroll
-        for (int i = 0; i < kAgain; ++i) {
-            const int64_t j = from + i * kThreads + tid;
-            at[i] = -1;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (j < total) {
-                const int32_t e = total <= INT32_MAX ? (int32_t)j / per : (int32_t)(j / per);
-                const int32_t g = sh.list[e], vec = g / kThreads * per + (int32_t)(j - (int64_t)e * per);
-                const int32_t q = (vec >> 1) * kThreads + g % kThreads;  // its sector
-                if ((vec >> 1) < sl.steps * kSecs && q >= sl.whole0 && q < sl.whole1) {
-                    at[i] = 2 * q + (vec & 1);
-                    v[i] = __ldg(static_cast<const uint4*>(sl.base) + at[i]);
-                }
-            }
+    for (int half = 0; half < (halves ? 2 : 1); ++half) {
+        if (half) {
+            mine = rest;
+            count(mine);
         }
-        from += kAgain * kThreads;
-        int done = 0;  // vectors of this warp that are through
-        bool again;
+        for (; mine; mine &= mine - 1) sh.list[place++] = (uint16_t)((__ffs(mine) - 1) * kThreads + tid);
+        __syncthreads();
+        const int64_t total = (int64_t)n_list * per;
+        int64_t from = 0;
 #pragma unroll 1
         do {
-            int32_t room = kWarpRoom;
-#pragma unroll 1
-            for (; done < kAgain; ++done) {
-                uint4 x = v[0];
-                int32_t q = at[0];
+            uint4 v[kAgain];
+            int32_t at[kAgain];  // 16-byte vector of the slice, or -1
 #pragma unroll
-                for (int i = 1; i < kAgain; ++i)
-                    if (done == i) {
-                        x = v[i];
-                        q = at[i];
-                    }
-                float most = element<E>(x, 0);
-#pragma unroll
-                for (int e = 1; e < kN; ++e) most = fmaxf(most, element<E>(x, e));
-                const bool hot = q >= 0 && most >= limit;
-                const uint32_t who = __ballot_sync(0xffffffffu, hot);
-                if (who == 0) continue;
-                if (__popc(who) * kN > room) break;  // the rest after a merge
-                int n = 0;
-                if (hot) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) {
-                        if (!(element<E>(x, e) >= limit)) continue;
-                        const Key key = make_key(element<E>(x, e), (uint32_t)(sl.id0 + q * kN + e));
-                        if (key > bound) {
-                            put(sh, key);
-                            ++n;
-                        }
+            for (int i = 0; i < kAgain; ++i) {
+                const int64_t j = from + i * kThreads + tid;
+                at[i] = -1;
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (j < total) {
+                    const int32_t e = total <= INT32_MAX ? (int32_t)j / per : (int32_t)(j / per);
+                    const int32_t g = sh.list[e], vec = g / kThreads * per + (int32_t)(j - (int64_t)e * per);
+                    const int32_t q = (vec >> 1) * kThreads + g % kThreads;  // its sector
+                    if ((vec >> 1) < sl.steps * kSecs && q >= sl.whole0 && q < sl.whole1) {
+                        at[i] = 2 * q + (vec & 1);
+                        v[i] = __ldg(static_cast<const uint4*>(sl.base) + at[i]);
                     }
                 }
-                room -= __reduce_add_sync(0xffffffffu, n);
             }
-            again = __syncthreads_or(done < kAgain) != 0;
-            const bool full = sh.n_cand > kCand - kThreads / 32 * kWarpRoom;
-            __syncthreads();
-            if (full || (!again && from >= total)) {
-                merge(sh, k, tid);
-                bound = sh.bound;
-                if (bound) limit = fmaxf(limit, key_value(bound));
-            }
-        } while (again);
-    } while (from < total);
+            from += kAgain * kThreads;
+            int done = 0;  // vectors of this warp that are through
+            bool again;
+#pragma unroll 1
+            do {
+                int32_t room = kWarpRoom;
+#pragma unroll 1
+                for (; done < kAgain; ++done) {
+                    uint4 x = v[0];
+                    int32_t q = at[0];
+#pragma unroll
+                    for (int i = 1; i < kAgain; ++i)
+                        if (done == i) {
+                            x = v[i];
+                            q = at[i];
+                        }
+                    float most = element<E>(x, 0);
+#pragma unroll
+                    for (int e = 1; e < kN; ++e) most = fmaxf(most, element<E>(x, e));
+                    const bool hot = q >= 0 && most >= limit;
+                    const uint32_t who = __ballot_sync(0xffffffffu, hot);
+                    if (who == 0) continue;
+                    if (__popc(who) * kN > room) break;  // the rest after a merge
+                    int n = 0;
+                    if (hot) {
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) {
+                            if (!(element<E>(x, e) >= limit)) continue;
+                            const Key key = make_key(element<E>(x, e), (uint32_t)(sl.id0 + q * kN + e));
+                            if (key > bound) {
+                                put(sh, key);
+                                ++n;
+                            }
+                        }
+                    }
+                    room -= __reduce_add_sync(0xffffffffu, n);
+                }
+                again = __syncthreads_or(done < kAgain) != 0;
+                const bool full = sh.n_cand > kCand - kThreads / 32 * kWarpRoom;
+                __syncthreads();
+                if (full || (!again && from >= total)) {
+                    merge(sh, k, tid);
+                    bound = sh.bound;
+                    if (bound) limit = fmaxf(limit, key_value(bound));
+                }
+            } while (again);
+        } while (from < total);
+    }
 }
 
 // A shift of the maximum in the exponent. 2^-200 is 0; a longer shift would only make the products with it
@@ -341,16 +386,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     // element by element. Offsets within the slice fit 32 bits.
     const int32_t mis = (int32_t)((reinterpret_cast<uintptr_t>(r) & 31) / sizeof(E));
     const int64_t secs = ((int64_t)p.V + mis + kN - 1) / kN;
-    const int64_t per = (secs + p.slices - 1) / p.slices;
-    const int64_t q0 = min(secs, blockIdx.x * per);
-    const int32_t nq = (int32_t)(min(secs, q0 + per) - q0);
+    const int64_t q0 = secs * blockIdx.x / p.slices;
+    const int32_t nq = (int32_t)(secs * (blockIdx.x + 1) / p.slices - q0);
     const int32_t whole0 = q0 == 0 && mis ? 1 : 0;
     const int32_t whole1 = q0 + nq == secs && (p.V + mis) % kN ? nq - 1 : nq;
     const E* base = r + (q0 * kN - mis);
     const int32_t id0 = (int32_t)(q0 * kN) - mis;  // id of the slice's first element
     const float sl2 = kLog2e / p.temperature;
     if (tid == 0) {
-        sh.n_kept = sh.n_cand = sh.n_list = 0;
+        sh.n_kept = sh.n_cand = 0;
         sh.bound = 0;
     }
     // a given token's logit, fetched while the row streams
@@ -464,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
 #pragma unroll
                 for (int u = 0; u < 2 * kSecs; ++u) cur[u] = nxt[u];
             }
-            sh.group[phase][tid] = group;
+            sh.group[phase][tid] = __float2bfloat16_ru(group);
             top = fmaxf(top, group);
         }
     }
@@ -530,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
             } else if (tid / p.slices < k) {
                 top = __ldcg(keys + (int64_t)(tid % p.slices) * k + tid / p.slices);
             }
-            raise_bound(sh, k, tid, top);
+            const Key least = bound_of(sh.warp_key, k, tid, top, Key(0));
+            if (tid == 0 && least > 0) sh.bound = least - 1;  // the key itself stays in
+            __syncthreads();
             for (int64_t at = 0; at < total; at += 4 * kThreads) {
                 const Key bound = sh.bound;
                 Key mine[4];

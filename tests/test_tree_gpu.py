@@ -622,6 +622,28 @@ def test_logprobs_many_rows_match_torch():
     assert ((ent + (want.exp() * want).sum(1)).abs() <= 32 * tol).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_logprobs_long_slices_of_equal_and_ordered_values(dtype):
+    # enough rows for one slice each, of more than 16 steps: every group of equal values is read again
+    R, V, k = 700, 70001, 64
+    g = torch.Generator(device="cuda").manual_seed(54)
+    x = torch.randn((R, V), generator=g, device="cuda").to(dtype)
+    x[0::7] = 1.5
+    x[1::7] = -torch.inf
+    x[2::7] = torch.where(torch.arange(V, device="cuda") % 3 == 1, 2.0, -1.0).to(dtype)
+    x[3::7] = torch.arange(V, device="cuda").to(dtype)
+    x[4::7] = -torch.arange(V, device="cuda").to(dtype)
+    x[5::7, 40000:] = 5.0
+    _, _, z, top, lp = dfl.token_logprobs(x, top_k=k)
+    assert torch.equal(z[0::7], torch.full_like(z[0::7], 1).fill_(z[0].item()))
+    for r in list(range(14)) + [R - 1]:
+        sv, si = x[r].double().sort(descending=True, stable=True)
+        assert torch.equal(top[r].long(), si[:k]), r
+        want = sv[:k] - torch.logsumexp(x[r].double(), 0) if torch.isfinite(sv[0]) else sv[:k]
+        # values of up to 70000 less a maximum of their size, exact; ln s to a few roundings of values below 16
+        assert ((lp[r].double() - want).nan_to_num(0.0).abs() <= 2.0 ** -17).all(), r
+
+
 def test_logprobs_repeats_streams_and_graphs():
     # several slices a row, other sizes in between, and graphs whose workspaces are their own
     g = torch.Generator(device="cuda").manual_seed(51)

@@ -4,11 +4,13 @@
 // Pairs that one range holds whole are final already. A request with a bad length or tree size gets its
 // zeros here.
 //
-// A warp takes a row: its lanes read the partials' lse values (32 at a time) and form the weights while the first
-// partial rows come, four to sixteen a time (2 requests of 2000 keys, 12 nodes of 8/2 heads, D = 64: 36 parts a row, 9.4
-// us by itself with sixteen, 13.3 with four). Launched as a programmatic dependent of the attention kernel; the deal
-// of tiles to ranges is worked out before the wait for it. Bound: trips to L2, two to start with and one more per batch
-// of partials; behind the attention it adds 4 to 7 us.
+// A warp takes a row, or where there are few rows 2, 4 or 8 warps take one, a stretch of its partials each, and add
+// theirs up in shared memory, in order. A warp's lanes read the partials' lse values (32 at a time) and form the weights
+// while the first partial rows come, four to sixteen a time. Launched as a programmatic dependent of the attention
+// kernel; the deal of tiles to ranges is worked out before the wait for it. Bound: trips to L2, two to start with and
+// one more per batch of partials; behind the attention it adds 3 to 7 us. Measured, whole calls of one request: 1 node,
+// 16/1 heads of 128, 100k keys (151 partials a row) 33 us, 51 with a warp per row; 7 nodes, 12/2 heads of 96, 18k keys
+// 22.5, 41 with a warp per row.
 #include <algorithm>
 #include <cmath>
 
@@ -20,10 +22,18 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-template <int V>  // floats per lane: DV <= 32 V
-__global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParams p)
+// Partials whose loads a warp has in flight, of V floats a lane, and the CTAs that an SM then holds.
+template <int V>
+constexpr int kAheadOf = V == 2 ? 16 : V == 8 ? 8 : 4;
+template <int V>
+constexpr int kCtasOf = V == 4 ? 4 : 2;
+
+template <int V, bool kShare>  // floats per lane: DV <= 32 V; several warps to a row
+__global__ void __launch_bounds__(kThreads, kCtasOf<V>)
+    tree_join_kernel(const TreeAttnParams p, const int32_t warps_a_row)
 {
     __shared__ int32_t sh_r0, sh_parts;
+    __shared__ float sh_acc[kShare ? kWarps : 1][V][32], sh_m[kWarps], sh_t[kWarps];
     const int32_t pair = blockIdx.x;
     const int32_t b = pair / p.Hkv, g = pair % p.Hkv;
     const int32_t sub = blockIdx.y;
@@ -57,12 +67,21 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
     constexpr int kRun = V < 4 ? 2 : 4;
     const int32_t d0 = lane * kRun;
     auto dim_of = [&](int u) -> int32_t { return d0 + u / kRun * 128; };  // of run u / kRun
-    const int32_t one = min(parts, 32);
-    for (int32_t row = blockIdx.z * kWarps + warp; row < live; row += gridDim.z * kWarps) {
+    const int32_t share = kShare ? warps_a_row : 1;
+    // `share` warps to a row: this one's partials are [c0, c1). No fewer than it loads at once, so that few partials
+    // are one warp's.
+    constexpr int kAhead = kAheadOf<V>;
+    const int32_t member = warp % share, rows_here = kWarps / share, per = kShare ? max(kAhead, (parts + share - 1) / share) : parts;
+    const int32_t c0 = min(parts, member * per), c1 = min(parts, c0 + per);
+    const int32_t one = min(c1 - c0, 32);
+    for (int32_t row0 = blockIdx.z * rows_here; row0 < live; row0 += gridDim.z * rows_here) {
+        const int32_t row = row0 + warp / share;
+        if (!kShare && row >= live) break;
+        const bool on_row = !kShare || row < live;
         // part c's row: the pair's first part is in slot 1 of its range, the others in slot 0
         auto part_at = [&](int32_t c) -> int64_t { return tree_part_row(p, r0 + c, sub, c == 0 ? 1 : 0) + row; };
         auto load = [&](int32_t c, bool live_part, float (&x)[V]) {
-            const float* src = p.part_out + part_at(live_part ? c : 0) * p.DV;
+            const float* src = p.part_out + part_at(live_part ? c : c0) * p.DV;
 #pragma unroll
             for (int u = 0; u < V; u += kRun) {
                 const bool on = live_part && dim_of(u) < d_here;
@@ -82,20 +101,19 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
             }
         };
         // The first parts' values are on their way beside the lse values that weigh them: one trip to L2, mostly.
-        constexpr int kAhead = V == 2 ? 16 : V == 8 ? 8 : 4;
         float lse0 = -INFINITY, ahead[kAhead][V];
-        if (parts > 0) {
-            lse0 = lane < one ? __ldcg(p.part_lse + part_at(lane)) : -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) load(k, k < parts, ahead[k]);
-        }
-        float m = lse0;
-        for (int32_t c = 32 + lane; c < parts; c += 32) m = fmaxf(m, __ldcg(p.part_lse + part_at(c)));
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        float t = 0.f, acc[V];
+        float m = -INFINITY, t = 0.f, acc[V];
 #pragma unroll
         for (int u = 0; u < V; ++u) acc[u] = 0.f;
+        if (on_row && c0 < c1) {
+            lse0 = lane < one ? __ldcg(p.part_lse + part_at(c0 + lane)) : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) load(c0 + k, c0 + k < c1, ahead[k]);
+            m = lse0;
+            for (int32_t c = c0 + 32 + lane; c < c1; c += 32) m = fmaxf(m, __ldcg(p.part_lse + part_at(c)));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        }
         if (m != -INFINITY) {
             // (a partial without a visible key is 0 and so is its weight)
             float w = lse0 == -INFINITY ? 0.f : expf(lse0 - m);
@@ -106,22 +124,46 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
 #pragma unroll
                 for (int u = 0; u < V; ++u) acc[u] = fmaf(wk, ahead[k][u], acc[u]);
             }
-            for (int32_t c1 = kAhead; c1 < parts; c1 += kAhead) {
-                if (c1 % 32 == 0) {
-                    const float l = c1 + lane < parts ? __ldcg(p.part_lse + part_at(c1 + lane)) : -INFINITY;
+            for (int32_t at = kAhead; c0 + at < c1; at += kAhead) {
+                if (at % 32 == 0) {
+                    const int32_t c = c0 + at + lane;
+                    const float l = c < c1 ? __ldcg(p.part_lse + part_at(c)) : -INFINITY;
                     w = l == -INFINITY ? 0.f : expf(l - m);
                 }
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) load(c1 + k, c1 + k < parts, ahead[k]);
+                for (int k = 0; k < kAhead; ++k) load(c0 + at + k, c0 + at + k < c1, ahead[k]);
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
-                    const float wk = __shfl_sync(0xffffffffu, w, (c1 + k) & 31);
+                    const float wk = __shfl_sync(0xffffffffu, w, (at + k) & 31);
                     t += wk;
 #pragma unroll
                     for (int u = 0; u < V; ++u) acc[u] = fmaf(wk, ahead[k][u], acc[u]);
                 }
             }
         }
+        if (kShare && per < parts) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) sh_acc[warp][u][lane] = acc[u];
+            if (lane == 0) {
+                sh_m[warp] = m;
+                sh_t[warp] = t;
+            }
+            __syncthreads();
+            if (member == 0) {
+                for (int i = 1; i < share; ++i) m = fmaxf(m, sh_m[warp + i]);
+                t = 0.f;
+#pragma unroll
+                for (int u = 0; u < V; ++u) acc[u] = 0.f;
+                for (int i = 0; i < share; ++i) {
+                    const float mi = sh_m[warp + i], wi = mi == -INFINITY ? 0.f : expf(mi - m);
+                    t = fmaf(wi, sh_t[warp + i], t);
+#pragma unroll
+                    for (int u = 0; u < V; ++u) acc[u] = fmaf(wi, sh_acc[warp + i][u][lane], acc[u]);
+                }
+            }
+            __syncthreads();
+        }
+        if (member != 0 || !on_row) continue;
         const bool empty = !(t > 0.f);
         const float inv = empty ? 0.f : 1.f / t;
         const int32_t node = node0 + row / p.Gc, head = g * p.G + st.gc * p.Gc + row % p.Gc;
@@ -144,12 +186,15 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(const TreeAttnParam
 
 }  // namespace
 
-cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream)
+template <int V>
+static cudaError_t launch_join(const TreeAttnParams& p, cudaStream_t stream)
 {
+    // about one wave of warps: a warp takes several rows of a large call, several warps take one of a small one
+    const int64_t wave = (int64_t)device_sm_count() * kCtasOf<V>, tiles = (int64_t)p.B * p.Hkv * p.n_sub;
+    int32_t share = 1;
+    while (share < kWarps && tiles * p.rows * share * 2 <= wave * kWarps) share *= 2;
+    const int64_t most = (p.rows * share + kWarps - 1) / kWarps;
     cudaLaunchConfig_t cfg = {};
-    // about one wave of warps: a warp then takes several rows of a large call, one of a small one
-    const int64_t wave = (int64_t)device_sm_count() * 4, tiles = (int64_t)p.B * p.Hkv * p.n_sub;
-    const int64_t most = (p.rows + kWarps - 1) / kWarps;
     cfg.gridDim = dim3((unsigned)(p.B * p.Hkv), (unsigned)p.n_sub,
                        (unsigned)std::max<int64_t>(1, std::min(most, (wave + tiles - 1) / tiles)));
     cfg.blockDim = dim3(kThreads);
@@ -159,11 +204,17 @@ cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return share > 1 ? cudaLaunchKernelEx(&cfg, tree_join_kernel<V, true>, p, share)
+                     : cudaLaunchKernelEx(&cfg, tree_join_kernel<V, false>, p, share);
+}
+
+cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream)
+{
     // a lane's floats: the narrowest that cover the partial's row (DV is a multiple of 16)
-    if (p.DV <= 64) return cudaLaunchKernelEx(&cfg, tree_join_kernel<2>, p);
-    if (p.DV <= 128) return cudaLaunchKernelEx(&cfg, tree_join_kernel<4>, p);
-    if (p.DV <= 256) return cudaLaunchKernelEx(&cfg, tree_join_kernel<8>, p);
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<16>, p);
+    if (p.DV <= 64) return launch_join<2>(p, stream);
+    if (p.DV <= 128) return launch_join<4>(p, stream);
+    if (p.DV <= 256) return launch_join<8>(p, stream);
+    return launch_join<16>(p, stream);
 }
 
 }  // namespace dflash

@@ -242,6 +242,15 @@ def test_long_contexts_in_many_ranges(kernel, dtype, d, hq, hkv):
 
 
 @pytest.mark.parametrize("kernel,dtype", BOTH)
+@pytest.mark.parametrize("d", [48, 128, 256, 512])
+@pytest.mark.parametrize("nodes,hq,hkv", [(1, 1, 1), (3, 8, 2)])
+def test_few_rows_in_many_ranges(kernel, dtype, d, nodes, hq, hkv):
+    # up to a partial per CTA of the GPU for each row
+    t = Tree([nodes], [31003], hq=hq, hkv=hkv, d=d, dtype=dtype, seed=55)
+    t.check(*t.call(kernel))
+
+
+@pytest.mark.parametrize("kernel,dtype", BOTH)
 def test_scores_far_apart(kernel, dtype):
     # scores of some hundreds: later tiles raise the maximum and rescale the accumulators many times
     t = Tree([16, 16], [900, 1500], hq=8, hkv=2, d=128, dtype=dtype, seed=9)

@@ -39,6 +39,7 @@ struct TreeAttnParams {
     int32_t Gc, npt, nrt, ndv, rows, DV, n_sub, ranges;
     int32_t pair;  // 1: tensor-core CTA pairs; neighbouring node tiles are neighbouring query tiles
     int32_t tile;  // keys per tile
+    int32_t pair_cost;  // of a pair beside its tiles, in tiles
     unsigned long long wait_ns;
 };
 

@@ -93,6 +93,9 @@ void tree_attn_plan(TreeAttnParams& p, int kernel)
     p.npt = (p.T + p.nrt - 1) / p.nrt;  // node tiles of equal size
     p.rows = p.npt * p.Gc;
     p.tile = tc ? 128 : 64;
+    // A pair's fixed cost: some 4 us, of tiles of about 1 us on the tensor cores and of rows x dims / 2500 us on the
+    // CUDA cores (fp32, 8 requests of 150 keys, 26 nodes, 32/4 heads of 512: 184 us with 4 tiles, 164 with none).
+    p.pair_cost = tc ? 4 : std::min(4, 10000 / (std::max(16, p.rows) * p.D));
     p.DV = !tc ? p.D : p.D <= 64 && !p.pair ? 64 : p.D <= 128 ? 128 : 256;
     p.ndv = (p.D + p.DV - 1) / p.DV;
     p.n_sub = (p.G / p.Gc) * p.nrt * p.ndv;

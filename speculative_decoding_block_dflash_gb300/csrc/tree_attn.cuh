@@ -40,12 +40,13 @@ __device__ __forceinline__ uint32_t tree_request_error(const TreeAttnParams& p, 
     return (r.n < 0 || r.n > p.T) ? DFLASH_DEVERR_TREE : DFLASH_DEVERR_SEQ_LEN;
 }
 
-// The deal counts in units of a key tile's time. A pair of nt tiles weighs kPairCost + nt: its first units stand for
+// The deal counts in units of a key tile's time. A pair of nt tiles weighs pair_cost + nt: its first units stand for
 // loading its queries, filling the pipeline and writing its result, so that ranges of many short pairs get fewer
 // tiles.
-constexpr int32_t kPairCost = 4;
-
-__device__ __forceinline__ int64_t tree_weight(const TreeReq& r) { return r.nt > 0 ? r.nt + kPairCost : 0; }
+__device__ __forceinline__ int64_t tree_weight(const TreeAttnParams& p, const TreeReq& r)
+{
+    return r.nt > 0 ? r.nt + p.pair_cost : 0;
+}
 
 // Weight of all (request, KV head) pairs before request b (b = B: of all). Called by a whole warp.
 __device__ __forceinline__ int64_t tree_weight_before(const TreeAttnParams& p, int32_t b_end)
@@ -53,7 +54,7 @@ __device__ __forceinline__ int64_t tree_weight_before(const TreeAttnParams& p, i
     const int lane = threadIdx.x & 31;
     int64_t sum = 0;
 #pragma unroll 1
-    for (int32_t b = lane; b < b_end; b += 32) sum += tree_weight(tree_request(p, b));
+    for (int32_t b = lane; b < b_end; b += 32) sum += tree_weight(p, tree_request(p, b));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     return sum * p.Hkv;
@@ -93,12 +94,12 @@ struct PieceWalk {
     int32_t t0, t1;    // the piece: tiles [t0, t1) of the pair's
     TreeReq req;
 
-    __device__ __forceinline__ void cut()
+    __device__ __forceinline__ void cut(const TreeAttnParams& p)
     {
-        const int64_t weight = tree_weight(req);
+        const int64_t weight = tree_weight(p, req);
         const int64_t end = left < weight - at ? at + left : weight;
-        t0 = max(0, at - kPairCost);
-        t1 = max(0, (int32_t)end - kPairCost);
+        t0 = max(0, at - p.pair_cost);
+        t1 = max(0, (int32_t)end - p.pair_cost);
         left -= end - at;
     }
     __device__ __forceinline__ bool done() const { return t1 <= t0; }
@@ -112,7 +113,7 @@ struct PieceWalk {
         req.bad = false;
         // the first 32 requests, a lane each: all there are, mostly
         const TreeReq own = lane < p.B ? tree_request(p, lane) : req;
-        int64_t mine = tree_weight(own) * p.Hkv;
+        int64_t mine = tree_weight(p, own) * p.Hkv;
         int64_t total = mine;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
@@ -126,7 +127,7 @@ struct PieceWalk {
         if (left <= 0) return;
 #pragma unroll 1
         for (int32_t b0 = 0;; b0 += 32) {
-            if (b0 > 0) mine = b0 + lane < p.B ? tree_weight(tree_request(p, b0 + lane)) * p.Hkv : 0;
+            if (b0 > 0) mine = b0 + lane < p.B ? tree_weight(p, tree_request(p, b0 + lane)) * p.Hkv : 0;
             int64_t incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -156,9 +157,9 @@ struct PieceWalk {
         } else {
             req = tree_request(p, b);
         }
-        g = (int32_t)div_small(x, tree_weight(req));
-        at = (int32_t)(x - g * tree_weight(req));
-        cut();
+        g = (int32_t)div_small(x, tree_weight(p, req));
+        at = (int32_t)(x - g * tree_weight(p, req));
+        cut(p);
         if (done()) next(p);  // the range begins in a pair's first units and ends there, or it does not reach a tile
     }
     // The next piece that holds a tile, if any (done() otherwise).
@@ -177,7 +178,7 @@ struct PieceWalk {
                     req = tree_request(p, b);
                 } while (req.nt == 0);
             }
-            cut();
+            cut(p);
         }
     }
     // Whether the piece is a whole pair (its result is final), and its partial's slot otherwise: the pair's

@@ -48,11 +48,11 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<V>)
     int32_t r0 = 0, parts = 0;
     if (rq.nt > 0 && live > 0) {
         if (warp == 0) {
-            const int64_t first = tree_weight_before(p, b) + g * tree_weight(rq), total = tree_weight_before(p, p.B);
+            const int64_t first = tree_weight_before(p, b) + g * tree_weight(p, rq), total = tree_weight_before(p, p.B);
             const int32_t used = ranges_used(p, total);
             if (lane == 0) {
-                sh_r0 = range_of(total, used, first + kPairCost);  // its tiles follow its fixed cost
-                sh_parts = range_of(total, used, first + tree_weight(rq) - 1) - sh_r0 + 1;
+                sh_r0 = range_of(total, used, first + p.pair_cost);  // its tiles follow its fixed cost
+                sh_parts = range_of(total, used, first + tree_weight(p, rq) - 1) - sh_r0 + 1;
             }
         }
         __syncthreads();

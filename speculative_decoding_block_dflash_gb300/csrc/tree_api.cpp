@@ -87,8 +87,11 @@ void tree_attn_plan(TreeAttnParams& p, int kernel)
         }
     const int32_t fit = most / p.Gc;
     p.nrt = (p.T + fit - 1) / fit;
-    // several node tiles on the tensor cores: CTA pairs, an even number of tiles
-    p.pair = tc && p.nrt > 1 ? 1 : 0;
+    // Several node tiles on the tensor cores: CTA pairs, an even number of tiles. Of up to 64 dims, where a pair's MMAs
+    // are half empty, an odd number stays as it is (4 requests of 4k to 9k keys, 32/8 heads of 64: 90 nodes, 3 tiles,
+    // 55 us against 66 in pairs; 128 nodes, 4 tiles, 72 against 68; of 128 dims and more pairs take 0.7 to 0.9 of the
+    // time for 3 tiles too).
+    p.pair = tc && p.nrt > 1 && (p.D > 64 || p.nrt % 2 == 0) ? 1 : 0;
     if (p.pair) p.nrt = (p.nrt + 1) / 2 * 2;
     p.npt = (p.T + p.nrt - 1) / p.nrt;  // node tiles of equal size
     p.rows = p.npt * p.Gc;

@@ -169,7 +169,8 @@ def test_head_layouts(kernel, dtype, hq, hkv):
 
 @pytest.mark.parametrize("kernel,dtype", BOTH)
 @pytest.mark.parametrize("T,hq,hkv,d", [(1, 8, 2, 128), (2, 4, 4, 64), (33, 8, 2, 128), (64, 8, 1, 128), (65, 8, 2, 256),
-                                        (128, 4, 1, 64), (200, 6, 2, 128), (256, 2, 1, 512), (256, 4, 2, 128)])
+                                        (128, 4, 1, 64), (200, 6, 2, 128), (256, 2, 1, 512), (256, 4, 2, 128),
+                                        (90, 8, 2, 64), (95, 4, 1, 48), (157, 8, 2, 32)])
 def test_tree_sizes(kernel, dtype, T, hq, hkv, d):
     nodes = [T, max(1, T // 2)]
     t = Tree(nodes, [nodes[0] + 200, nodes[1] + 1], T=T, hq=hq, hkv=hkv, d=d, dtype=dtype, seed=T)

@@ -6,14 +6,16 @@
 // A CTA of 256 threads owns a tile of up to 64 query rows (node x head) and streams its range's key tiles of 64
 // keys once. Products are register-tiled: a thread holds R rows x 4 keys of the scores and R rows x 4 dims of
 // every 64-dim chunk of the output, so each value read from shared memory feeds R to 4 R FMAs; R is 4, or 2 or
-// 1 where a KV head has no more than 32 or 16 rows (a single token's rows in tiles of 64 took 335 us for 4
-// requests of 8192 keys, all but 6 % of the FMAs on dead rows). K and V pass through two shared buffers of 64
-// keys x 64 dims (widened to fp32); the next chunk's global loads are in flight in registers while the current
-// one is used, and one barrier per chunk is enough. The softmax is online: running maximum and sum per row in
-// fp32, replicated over the row's 16 threads. Bound: the FMA pipe for full tiles (2 D FMAs per row and key
-// against 8 D bytes per key shared by 64 rows), the loads in flight for few rows. Measured, fp32, 4 requests of
-// 8192 keys, 32/8 heads of 128: 64 nodes 1290 us (24 TFLOP/s), 16 nodes 336 (23), 1 node 207 (1.3 TB/s); 2
-// requests of 4096 keys, 16 nodes, 32/4 heads of 512 341 (24 TFLOP/s), 32/16 heads of 256 253 (16).
+// 1 where a KV head has no more than 32 or 16 rows, and warps whose rows hold no node only load (one node's 4
+// rows a KV head, 4 requests of 8192 keys, D = 128: 335 us in tiles of 64, 207 of 16, 111 with the idle warps
+// out of shared memory's way). K and V pass through two shared buffers of 64 keys x 64 dims (widened to fp32);
+// the next chunk's global loads are in flight in registers while the current one is used, and one barrier per
+// chunk is enough. The softmax is online: running maximum and sum per row in fp32, replicated over the row's 16
+// threads. Bound: shared memory's bandwidth for full tiles (24 wavefronts per 64 FMAs of a warp), the loads in
+// flight for few rows. Measured, fp32, 4 requests of 8192 keys, 32/8 heads of 128: 64 nodes 1270 us (24
+// TFLOP/s), 16 nodes 335 (23), 1 node 111 (2.4 TB/s); 2 requests of 4096 keys, 16 nodes, 32/4 heads of 512 312
+// (26 TFLOP/s), 32/16 heads of 256 236 (17). (Tiles of 128 rows reach 29 TFLOP/s at D = 128, but one request of
+// 300 keys takes 55 us in place of 41.)
 #include <cmath>
 
 #include "tree_attn.cuh"
@@ -111,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas_per_sm(NC * 64, 16 * R))
         tree_walk_nodes(p, w.req, node0, min(p.npt, n - node0), par_s, anc_s, lo_s, tid, kThreads);
         // (the first chunk's barrier below makes the walk's results visible before the first mask)
 
+        const bool idle = (tid >> 5) * 2 * R >= live;  // this warp's rows have no node: it only loads
         float o[NC][R][4], m[R], l[R];
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas_per_sm(NC * 64, 16 * R))
                     fetch16(p, p.k, off, off >= 0, (c + 1) * 64 + ld0, nxt);
                 else
                     fetch16(p, p.v, off, off >= 0, ld0, nxt);
+                if (idle) continue;
 #pragma unroll 4
                 for (int d = 0; d < 64; d += 4) {
                     float4 qv[R], kv[4];
@@ -186,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas_per_sm(NC * 64, 16 * R))
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int row = ty * R + i;
+                if (idle) continue;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -227,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas_per_sm(NC * 64, 16 * R))
                     fetch16(p, p.v, off, off >= 0, (c + 1) * 64 + ld0, nxt);
                 else
                     fetch16(p, p.k, next_off, next_off >= 0, ld0, nxt);
+                if (idle) continue;
 #pragma unroll
                 for (int i = 0; i < R; ++i)
 #pragma unroll

@@ -19,7 +19,7 @@
 // time depends on the data: a row of equal logits reads every group again. A thread's values of a step are
 // whole sectors, so that reading a group again fetches little beside it. Measured, k = 64 beside none: 1000
 // rows of 151937 fp32 129 and 107 us (floor 90), bf16 82 and 67 (45); 4000 rows of 32000 bf16 100 and 61 (38);
-// 8 rows of 151936 bf16 27 and 10. (Candidates picked step by step, with a sort of 256 per merge, took 460 us
+// 8 rows of 151936 bf16 22 and 10. (Candidates picked step by step, with a sort of 256 per merge, took 460 us
 // for the first, with merges by rank at every doubling of what has been seen 143, with 16 groups a thread in
 // place of 32 137. A bound from all four warps alone, and a short last slice, took 43 us for the 8 rows: a warp
 // without values left no bound.)
@@ -563,8 +563,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
                 sh.bound = 0;
             }
             __syncthreads();
-            const int64_t total = (int64_t)p.slices * k;
-            const Key* keys = p.part_key + (int64_t)row * total;
+            const Key* keys = p.part_key + (int64_t)row * p.slices * k;
             // The slices' lists are in order, so their first keys (and, of fewer than 128 lists, their next few) give
             // a bound that leaves little more than k keys of them all; what exceeds it is merged. (Bounds from
             // keys a thread reads at stride 128 left thousands: every thread then sees one rank of all lists.)
@@ -577,22 +576,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
             const Key least = bound_of(sh.warp_key, k, tid, top, Key(0));
             if (tid == 0 && least > 0) sh.bound = least - 1;  // the key itself stays in
             __syncthreads();
-            for (int64_t at = 0; at < total; at += 4 * kThreads) {
-                const Key bound = sh.bound;
-                Key mine[4];
+            // Eight keys of each list a time, until no list goes on above the bound: mostly once (1 row of 151936, k = 64:
+            // 75 lists, 18.5 us in place of 24 with all of them).
+            bool more = true;
+            for (int32_t first = 0; first < k && more; first += 8) {
+                const int32_t width = min(8, k - first), total = p.slices * width;
+                bool goes_on = false;
+                for (int32_t at = 0; at < total; at += 4 * kThreads) {
+                    const Key bound = sh.bound;
+                    Key mine[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t j = at + i * kThreads + tid;
-                    mine[i] = j < total ? __ldcg(keys + j) : 0;
+                    for (int i = 0; i < 4; ++i) {
+                        const int32_t j = at + i * kThreads + tid, list = j / width, place = j - list * width;
+                        mine[i] = j < total ? __ldcg(keys + (int64_t)list * k + first + place) : 0;
+                        goes_on = goes_on || (place == width - 1 && mine[i] > bound);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (mine[i] > bound) put(sh, mine[i]);
+                    const bool last = at + 4 * kThreads >= total;
+                    __syncthreads();
+                    const bool full = sh.n_cand > kCand - 4 * kThreads;
+                    __syncthreads();
+                    if (full || last) merge(sh, k, tid);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (mine[i] > bound) put(sh, mine[i]);
-                const bool last = at + 4 * kThreads >= total;
-                __syncthreads();
-                const bool full = sh.n_cand > kCand - 4 * kThreads;
-                __syncthreads();
-                if (full || last) merge(sh, k, tid);
+                more = __syncthreads_or(goes_on) != 0;
             }
         }
         if (tid == 0) p.counters[row] = 0;

@@ -606,6 +606,8 @@ def _call_on(dev: torch.device, stream):
 
 
 _tree_ws = {}
+# tree_attn launches two kernels that share a workspace: another thread's call on the stream must not come between.
+_tree_attn_lock = threading.Lock()
 
 
 def _tree_workspace(op: str, dev: torch.device, stream: int, nbytes: int, zeroed: int) -> torch.Tensor:
@@ -829,11 +831,12 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
             out = fresh(qs, dtype=q.dtype, device=dev)
         if lse is None and want_lse:
             lse = fresh(qs[:2], dtype=torch.float32, device=dev)
-        st = lib.dflash_tree_attn(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, parents_at, nodes_at,
-            dims_ref, T, window, 1.0 / math.sqrt(qs[2]) if scale is None else scale, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), KERNELS[kernel],
-            None if workspace is None else workspace.data_ptr(), nbytes, wait_limit_us, handle)
+        with _tree_attn_lock:
+            st = lib.dflash_tree_attn(
+                q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, parents_at, nodes_at,
+                dims_ref, T, window, 1.0 / math.sqrt(qs[2]) if scale is None else scale, out.data_ptr(),
+                None if lse is None else lse.data_ptr(), KERNELS[kernel],
+                None if workspace is None else workspace.data_ptr(), nbytes, wait_limit_us, handle)
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)

@@ -10,6 +10,8 @@ probabilities, A = sum_j p_j |v_j| and S = the largest scale * sum_d |q_d k_d| o
   * sums over n keys in fp32: n u32 A (and n u32 for the lse);
   * the output's own rounding: u |o|.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -368,6 +370,33 @@ def test_same_bits_twice_on_streams_and_in_graphs(kernel, dtype):
         torch.cuda.synchronize()
         for w, g in zip(want, outs):
             torch.testing.assert_close(w, g, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("kernel,dtype", BOTH)
+def test_threads_that_share_a_stream(kernel, dtype):
+    # two threads' calls on one stream, whose workspace they share
+    cases = [Tree([9, 4], [900, 1300], hq=8, hkv=2, d=128, dtype=dtype, seed=56),
+             Tree([3], [2500], hq=8, hkv=2, d=64, dtype=dtype, seed=57)]
+    calls = []
+    for t in cases:
+        args = (torch.from_numpy(t.table).cuda(), torch.tensor(t.lens, dtype=torch.int32, device="cuda"),
+                torch.from_numpy(t.parents).cuda(), torch.tensor(t.nodes, dtype=torch.int32, device="cuda"))
+        calls.append(lambda t=t, a=args: dfl.tree_attn(t.q, t.k, t.v, a[0], a[1], a[2], num_nodes=a[3], kernel=kernel))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        for _ in range(100):
+            got = [calls[i]() for _ in range(4)]
+            bad.extend(i for g in got if not (torch.equal(g[0], want[i][0]) and torch.equal(g[1], want[i][1])))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
 
 
 @pytest.mark.parametrize("kernel", ["tc", "simt"])

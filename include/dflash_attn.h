@@ -489,7 +489,9 @@ DFLASH_API dflash_status dflash_token_logprobs(const void* logits, dflash_dtype 
  * and s, out and lse are those of dflash_block_attn. A chain (parents[i] = i - 1) is
  * dflash_block_attn with causal = 1.
  *
- *   q             device, [B*T, Hq, D] contiguous, dims->dtype; padding rows may hold anything.
+ *   q             device, [B*T, Hq, D] contiguous, dims->dtype; padding rows may hold anything. A row with
+ *                 a score of NaN or +inf, or whose scores are all -inf (q holds such values, or the products
+ *                 overflow fp32), comes out as NaN with a NaN lse; other rows are not touched by it.
  *   k_cache, v_cache, page_table   as in dflash_block_attn. Keys outside [first visible, L_b) are
  *                 never used, whatever they hold; pages without a visible key are not looked up. The
  *                 visible keys' K and V have to be finite (a node's K and V reach the

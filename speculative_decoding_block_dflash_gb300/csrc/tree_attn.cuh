@@ -2,6 +2,8 @@
 // ranges, and the ancestors of a tree's nodes.
 #pragma once
 
+#include <cmath>
+
 #include "dflash_device.cuh"
 #include "tree.h"
 
@@ -209,6 +211,29 @@ __device__ __forceinline__ SubTile sub_tile(const TreeAttnParams& p, int32_t sub
 __device__ __forceinline__ int64_t tree_part_row(const TreeAttnParams& p, int32_t range, int32_t sub, int slot)
 {
     return (((int64_t)range * p.n_sub + sub) * 2 + slot) * p.rows;
+}
+
+// What a row is scaled by, and its lse. A partial without a visible key has a sum of 0 and is all zeros, with lse -inf. A
+// row that has seen all of its keys, its own among them, has a sum of 0 only if every score was -inf: it is NaN, as one
+// with a score of NaN or +inf is, whose sum is NaN.
+__device__ __forceinline__ float tree_inv_sum(float sum, bool all_keys)
+{
+    if (sum != 0.f) return 1.f / sum;
+    return all_keys ? NAN : 0.f;
+}
+
+__device__ __forceinline__ float tree_row_lse(float lse, float sum, bool all_keys)
+{
+    if (sum != 0.f) return lse;
+    return all_keys ? NAN : -INFINITY;
+}
+
+// The larger value; NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // Parent of node i as the kernels use it: -1 where the table holds none or something out of range.

@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, simt_ctas_per_sm(NC * 64, 16 * R))
         for (int i = 0; i < R; ++i) {
             const int row = ty * R + i;
             if (row >= live) continue;
-            const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-            const float lse = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+            const float inv = tree_inv_sum(l[i], whole);
+            const float lse = tree_row_lse(m[i] + logf(l[i]), l[i], whole);
             const int32_t node = node0 + row / p.Gc, head = g * p.G + st.gc * p.Gc + row % p.Gc;
             const int64_t orow = ((int64_t)b * p.T + node) * p.Hq + head;
 #pragma unroll

@@ -800,9 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync_256();
             tc_fence_after();
             const float tot = ms.l[0][row] + ms.l[1][row];
-            const float inv = tot > 0.f ? 1.f / tot : 0.f;
+            const float inv = tree_inv_sum(tot, whole);
             if (live_row && half == 0) {
-                const float lse = tot > 0.f ? (m2 + __log2f(tot)) * kLn2 : -INFINITY;
+                const float lse = tree_row_lse((m2 + __log2f(tot)) * kLn2, tot, whole);
                 if (!whole)
                     p.part_lse[prow] = lse;
                 else if (p.lse && st.dv == 0)

@@ -1,6 +1,8 @@
 // Join of the tree attention's partials: a (request, KV head) pair whose key tiles lie in several
 // ranges has one normalised partial (o_c, lse_c) per range and row, and
 //   m = max_c lse_c, w_c = exp(lse_c - m), out = sum_c w_c o_c / sum_c w_c, lse = m + log(sum_c w_c).
+// A partial of scores that are not finite has a NaN lse; the maximum hands it on, so that the row is NaN as a whole pair's
+// would be.
 // Pairs that one range holds whole are final already. A request with a bad length or tree size gets its
 // zeros here.
 //
@@ -110,9 +112,9 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<V>)
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) load(c0 + k, c0 + k < c1, ahead[k]);
             m = lse0;
-            for (int32_t c = c0 + 32 + lane; c < c1; c += 32) m = fmaxf(m, __ldcg(p.part_lse + part_at(c)));
+            for (int32_t c = c0 + 32 + lane; c < c1; c += 32) m = max_nan(m, __ldcg(p.part_lse + part_at(c)));
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
         }
         if (m != -INFINITY) {
             // (a partial without a visible key is 0 and so is its weight)
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<V>)
             }
             __syncthreads();
             if (member == 0) {
-                for (int i = 1; i < share; ++i) m = fmaxf(m, sh_m[warp + i]);
+                for (int i = 1; i < share; ++i) m = max_nan(m, sh_m[warp + i]);
                 t = 0.f;
 #pragma unroll
                 for (int u = 0; u < V; ++u) acc[u] = 0.f;
@@ -164,8 +166,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<V>)
             __syncthreads();
         }
         if (member != 0 || !on_row) continue;
-        const bool empty = !(t > 0.f);
-        const float inv = empty ? 0.f : 1.f / t;
+        const float inv = tree_inv_sum(t, !rq.bad);
         const int32_t node = node0 + row / p.Gc, head = g * p.G + st.gc * p.Gc + row % p.Gc;
         const int64_t orow = ((int64_t)b * p.T + node) * p.Hq + head;
 #pragma unroll
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kCtasOf<V>)
                 *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) =
                     make_float2(acc[u] * inv, acc[u + 1] * inv);
         }
-        if (lane == 0 && st.dv == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : m + logf(t);
+        if (lane == 0 && st.dv == 0 && p.lse) p.lse[orow] = tree_row_lse(m + logf(t), t, !rq.bad);
     }
 }
 

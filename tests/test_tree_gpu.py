@@ -1100,3 +1100,35 @@ def test_a_captured_step_serves_other_lengths_and_trees(dtype):
                                         want[0], n)
             assert (cache.double().cpu().numpy() == moved).all()
         np.testing.assert_array_equal(lens.cpu().numpy(), new)
+
+
+# ------------------------------------------------------------------- scores that are not finite
+
+
+@pytest.mark.parametrize("kernel,dtype", BOTH)
+@pytest.mark.parametrize("kind", ["nan", "inf", "overflow", "lowest"])
+# one range; several ranges, of few rows (several warps to a row in the join) and of many
+@pytest.mark.parametrize("n,L,hq,hkv,d", [(5, 60, 4, 2, 64), (5, 3000, 4, 2, 64), (3, 9000, 2, 1, 512), (64, 3000, 32, 4, 128),
+                                          (40, 2500, 16, 2, 256)])
+def test_rows_of_scores_that_are_not_finite_come_out_as_nan(kernel, dtype, kind, n, L, hq, hkv, d):
+    # however the keys were dealt to ranges; and no other row changes a bit
+    t = Tree([n], [L], hq=hq, hkv=hkv, d=d, dtype=dtype, seed=60)
+    node, head = n - 1, hq - 1
+    if kind == "overflow":  # one key of the context gives a product above the largest fp32 number
+        page, slot = int(t.table[0, 3 // t.page]), 3 % t.page
+        t.k[page, slot] = 16.0
+    if kind == "lowest":  # every key does, below the lowest
+        live = torch.from_numpy(t.table[0][:-(-L // t.page)].copy()).long().cuda()
+        t.k[live] = t.k[live].abs() + 4.0
+    t.q[node, head] = 0.0
+    want, want_lse = t.call(kernel)
+    t.q[node, head] = {"nan": 0.0, "inf": 0.0, "overflow": 1e38, "lowest": -1e38}[kind]
+    if kind in ("nan", "inf"):
+        t.q[node, head, 3] = float(kind)
+    out, lse = t.call(kernel)
+    assert t.error() == 0
+    assert torch.isnan(out[node, head]).all() and torch.isnan(lse[node, head])
+    same = torch.ones((n, hq), dtype=torch.bool, device="cuda")
+    same[node, head] = False
+    assert torch.equal(out[same], want[same]) and torch.equal(lse[same], want_lse[same])
+    assert torch.isfinite(out[same].float()).all() and torch.isfinite(lse[same]).all()

@@ -72,7 +72,7 @@ extern "C" {
 #define DFLASH_API
 #endif
 
-#define DFLASH_ABI_VERSION 3
+#define DFLASH_ABI_VERSION 4
 #define DFLASH_MAX_HEAD_DIM 512
 #define DFLASH_MAX_BLOCK_LEN 64
 #define DFLASH_MAX_SPLITS 256
@@ -523,6 +523,22 @@ DFLASH_API dflash_status dflash_tree_attn(const void* q, const void* k_cache, co
                                           int32_t window, float scale, void* out, float* lse, dflash_kernel kernel,
                                           void* workspace, size_t workspace_bytes, uint32_t wait_limit_us,
                                           void* stream);
+
+/* dflash_tree_attn whose error bits are OR-ed into *device_error, a device uint32 word as the other tree calls take
+   it: the workspace's error word is then neither read nor written and need not be zeroed, so the workspace may
+   be scratch of the call alone (of a captured graph, say, that clears nothing). Such a word is read with a plain
+   copy: dflash_read_error would also clear 8 KB behind it after a timeout. NULL: dflash_tree_attn. */
+DFLASH_API dflash_status dflash_tree_attn_err(const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* page_table, const int32_t* seq_lens,
+                                              const int32_t* parents, const int32_t* num_nodes, const dflash_dims* dims,
+                                              int32_t max_nodes, int32_t window, float scale, void* out, float* lse,
+                                              dflash_kernel kernel, uint32_t* device_error, void* workspace,
+                                              size_t workspace_bytes, uint32_t wait_limit_us, void* stream);
+
+/* *word = the address of the library's own error word on the current device: zero when the library is loaded, there as
+   long as it is, for calls whose caller keeps none (the Python binding's captured tree attention). Read and
+   cleared by dflash_read_error, which takes it in place of a workspace (the block behind it is there). */
+DFLASH_API dflash_status dflash_shared_error_word(uint32_t** word);
 
 /*
  * Longest accepted path of drafted trees (dflash_accept_prefix for trees). With the target's token

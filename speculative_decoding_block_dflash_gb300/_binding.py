@@ -50,6 +50,8 @@ EXPORTED = (
     "dflash_token_logprobs",
     "dflash_tree_attn_workspace_bytes",
     "dflash_tree_attn",
+    "dflash_tree_attn_err",
+    "dflash_shared_error_word",
     "dflash_tree_accept_workspace_bytes",
     "dflash_tree_accept",
     "dflash_tree_commit",
@@ -165,6 +167,11 @@ def load_library(path: Optional[str] = None):
         lib.dflash_tree_attn.restype = ctypes.c_int
         lib.dflash_tree_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, dims_p, i32, i32, f32, vp, vp, i32, vp, size, u32,
                                          vp]
+        lib.dflash_tree_attn_err.restype = ctypes.c_int
+        lib.dflash_tree_attn_err.argtypes = [vp, vp, vp, vp, vp, vp, vp, dims_p, i32, i32, f32, vp, vp, i32, vp, vp,
+                                             size, u32, vp]
+        lib.dflash_shared_error_word.restype = ctypes.c_int
+        lib.dflash_shared_error_word.argtypes = [ctypes.POINTER(vp)]
         lib.dflash_tree_accept_workspace_bytes.restype = size
         lib.dflash_tree_accept_workspace_bytes.argtypes = []
         lib.dflash_tree_accept.restype = ctypes.c_int
@@ -615,7 +622,8 @@ def _tree_workspace(op: str, dev: torch.device, stream: int, nbytes: int, zeroed
     that calls that may overlap never share one. A call that is being captured gets its own, zeroed by the graph."""
     if torch._C._cuda_isCurrentStreamCapturing():
         buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        buf[:zeroed].zero_()
+        if zeroed:
+            buf[:zeroed].zero_()
         return buf
     key = (op, dev.index, stream)
     buf = _tree_ws.get(key)
@@ -623,6 +631,28 @@ def _tree_workspace(op: str, dev: torch.device, stream: int, nbytes: int, zeroed
         buf = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
         _tree_ws[key] = buf
     return buf
+
+
+# Words for the device errors of tree_attn calls whose caller gives none. They stand apart from the workspaces, which
+# grow and, of captured calls, belong to the graph.
+_tree_words = {}  # (device, stream) -> a word of its eager calls, in a block that dflash_read_error may clear
+_graph_words = {}  # device -> address of the word of its captured calls, the library's own
+_WORD_BLOCK = 256 + 8192
+
+
+def _tree_word(dev: torch.device, stream: int) -> int:
+    if torch._C._cuda_isCurrentStreamCapturing():
+        at = _graph_words.get(dev.index)
+        if at is None:
+            word = ctypes.c_void_p()
+            _check(load_library().dflash_shared_error_word(ctypes.byref(word)))
+            at = _graph_words[dev.index] = word.value
+        return at
+    word = _tree_words.get((dev.index, stream))
+    if word is None:
+        word = torch.zeros(_WORD_BLOCK, dtype=torch.uint8, device=dev)
+        word = _tree_words.setdefault((dev.index, stream), word)  # (another thread's, where that was first)
+    return word.data_ptr()
 
 
 def _bad(name: str, shape, dtype):
@@ -784,8 +814,8 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
               seq_lens: torch.Tensor, parents: torch.Tensor, num_nodes: Optional[torch.Tensor] = None, window: int = 0,
               scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
               kernel: str = "auto", workspace: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
-              stream=None, want_lse: bool = True,
-              wait_limit_us: int = 0) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+              stream=None, want_lse: bool = True, wait_limit_us: int = 0,
+              device_error: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Attention of drafted trees over a paged KV cache (dflash_tree_attn).
 
     q [B*T, Hq, D]; k_cache, v_cache [num_pages, page_size, Hkv, D] (head_dim contiguous), the nodes' own K/V
@@ -793,7 +823,8 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     [B, T] (-1 for a root, else an earlier node); num_nodes int32 [B] or None (T each). Returns
     (out [B*T, Hq, D] in q's dtype, lse fp32 [B*T, Hq] or None); padding rows of given outputs keep
     what they held, those of new ones are zero. Without a workspace the call uses one of its stream's (or the
-    captured graph's); its error word is read with tree_attn_error()."""
+    captured graph's). DEVERR_* bits go to device_error, an int32 device word, if given; else to the given workspace's
+    error word (read_error); else to a word that tree_attn_error() reads."""
     lib = _lib or load_library()
     qs, ps = q.shape, parents.shape
     if len(qs) != 3 or k_cache.dim() != 4 or len(ps) != 2:
@@ -818,6 +849,7 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
                             or lse.get_device() != index):
         _bad("lse", qs[:2], torch.float32)
     dims, dims_ref, nbytes = _tree_cache_dims(k_cache, v_cache, page_table, 0, qs[1], max_seq_len, T)
+    word = None if device_error is None else _check_word(device_error, index)
     if workspace is not None:
         nbytes = _check_ws(workspace, index)
     ctx, handle = _call_on(dev, stream)
@@ -826,16 +858,18 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     try:
         fresh = torch.empty if num_nodes is None else torch.zeros
         if workspace is None and nbytes:  # (0: sizes that the call itself refuses with the reason)
-            workspace = _tree_workspace("tree_attn", dev, handle, nbytes, 256)
+            workspace = _tree_workspace("tree_attn", dev, handle, nbytes, 0)
+            if word is None:
+                word = _tree_word(dev, handle)
         if out is None:
             out = fresh(qs, dtype=q.dtype, device=dev)
         if lse is None and want_lse:
             lse = fresh(qs[:2], dtype=torch.float32, device=dev)
         with _tree_attn_lock:
-            st = lib.dflash_tree_attn(
+            st = lib.dflash_tree_attn_err(
                 q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_at, lens_at, parents_at, nodes_at,
                 dims_ref, T, window, 1.0 / math.sqrt(qs[2]) if scale is None else scale, out.data_ptr(),
-                None if lse is None else lse.data_ptr(), KERNELS[kernel],
+                None if lse is None else lse.data_ptr(), KERNELS[kernel], word,
                 None if workspace is None else workspace.data_ptr(), nbytes, wait_limit_us, handle)
     finally:
         if ctx is not None:
@@ -846,15 +880,18 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
 
 
 def tree_attn_error(device=None, stream=None, clear: bool = True) -> int:
-    """The error word (DEVERR_* bits) of the workspace that tree_attn calls without one share on a stream;
-    synchronises the stream."""
+    """DEVERR_* bits of the tree_attn calls without a device_error and a workspace: of the stream's, and of the device's
+    captured ones, whatever stream replays them (a replay on another stream has to be waited for first); synchronises
+    the stream."""
     dev = torch.device("cuda" if device is None else device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     s = _stream_on(dev, stream)
     with torch.cuda.stream(s):
-        ws = _tree_ws.get(("tree_attn", dev.index, s.cuda_stream))
-        return 0 if ws is None else read_error(ws, clear=clear, stream=s)
+        word = _tree_words.get((dev.index, s.cuda_stream))
+        bits = 0 if word is None else _read_word(word.data_ptr(), clear, s.cuda_stream)
+        at = _graph_words.get(dev.index)
+        return bits if at is None else bits | _read_word(at, clear, s.cuda_stream)
 
 
 def tree_accept(logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor,
@@ -966,8 +1003,12 @@ def read_error(workspace: Optional[torch.Tensor] = None, clear: bool = True, str
         workspace = _ws_cache.get(("cuda", torch.cuda.current_device()))
         if workspace is None:
             return 0
+    return _read_word(workspace.data_ptr(), clear, _stream_handle(stream))
+
+
+def _read_word(at: int, clear: bool, stream: int) -> int:
     word = ctypes.c_uint32(0)
-    st = lib.dflash_read_error(workspace.data_ptr(), _stream_handle(stream), ctypes.byref(word), int(bool(clear)))
+    st = load_library().dflash_read_error(at, stream, ctypes.byref(word), int(bool(clear)))
     if st not in (OK, ERR_DEVICE_CHECK):
         _check(st)
     return int(word.value)

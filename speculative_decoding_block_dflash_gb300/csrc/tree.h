@@ -57,6 +57,8 @@ bool tree_tc_supports(const dflash_dims* d);
 cudaError_t launch_tree_attn_simt(const TreeAttnParams& p, cudaStream_t stream);
 cudaError_t launch_tree_attn_tc(TreeAttnParams& p, cudaStream_t stream);  // may take fewer ranges than planned
 cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream);
+// Address of the library's own error word on the current device; dflash_read_error may clear the block behind it.
+cudaError_t shared_error_word(uint32_t** word);
 
 // Log probabilities (csrc/token_logprobs.cu).
 struct LogprobsParams {

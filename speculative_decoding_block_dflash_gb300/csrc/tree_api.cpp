@@ -141,11 +141,11 @@ size_t dflash_tree_attn_workspace_bytes(const dflash_dims* dims, int32_t max_nod
     return need;
 }
 
-dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
-                               const int32_t* seq_lens, const int32_t* parents, const int32_t* num_nodes,
-                               const dflash_dims* dims, int32_t max_nodes, int32_t window, float scale, void* out,
-                               float* lse, dflash_kernel kernel, void* workspace, size_t workspace_bytes,
-                               uint32_t wait_limit_us, void* stream)
+dflash_status dflash_tree_attn_err(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                   const int32_t* seq_lens, const int32_t* parents, const int32_t* num_nodes,
+                                   const dflash_dims* dims, int32_t max_nodes, int32_t window, float scale, void* out,
+                                   float* lse, dflash_kernel kernel, uint32_t* device_error, void* workspace,
+                                   size_t workspace_bytes, uint32_t wait_limit_us, void* stream)
 {
     clear_error();
     const dflash_status s = check_attn_dims(dims, max_nodes, DFLASH_MAX_TREE_NODES, 1);
@@ -156,9 +156,9 @@ dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v
         return report_error(DFLASH_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
     if (out == q) return report_error(DFLASH_ERR_INVALID_ARG, "out must not alias q");
     if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(num_nodes, 4) ||
-        !aligned(lse, 4))
+        !aligned(lse, 4) || !aligned(device_error, 4))
         return report_error(DFLASH_ERR_INVALID_ARG,
-                            "page_table, seq_lens, parents, num_nodes and lse must be 4-byte aligned");
+                            "page_table, seq_lens, parents, num_nodes, lse and device_error must be 4-byte aligned");
     if (window < 0) return report_error(DFLASH_ERR_INVALID_ARG, "window %d < 0", window);
     if (!std::isfinite(scale) || !(scale > 0.f))
         return report_error(DFLASH_ERR_INVALID_ARG, "scale must be finite and > 0");
@@ -183,7 +183,7 @@ dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v
     p.num_nodes = num_nodes;
     p.out = out;
     p.lse = lse;
-    p.err = reinterpret_cast<uint32_t*>(wsb);
+    p.err = device_error ? device_error : reinterpret_cast<uint32_t*>(wsb);
     p.part_lse = reinterpret_cast<float*>(wsb + wl.lse_off);
     p.part_out = reinterpret_cast<float*>(wsb + wl.out_off);
     p.window = window;
@@ -195,6 +195,24 @@ dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v
     e = launch_tree_join(p, st);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention join launch");
     return DFLASH_OK;
+}
+
+dflash_status dflash_tree_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                               const int32_t* seq_lens, const int32_t* parents, const int32_t* num_nodes,
+                               const dflash_dims* dims, int32_t max_nodes, int32_t window, float scale, void* out,
+                               float* lse, dflash_kernel kernel, void* workspace, size_t workspace_bytes,
+                               uint32_t wait_limit_us, void* stream)
+{
+    return dflash_tree_attn_err(q, k_cache, v_cache, page_table, seq_lens, parents, num_nodes, dims, max_nodes, window,
+                                scale, out, lse, kernel, nullptr, workspace, workspace_bytes, wait_limit_us, stream);
+}
+
+dflash_status dflash_shared_error_word(uint32_t** word)
+{
+    clear_error();
+    if (!word) return report_error(DFLASH_ERR_INVALID_ARG, "NULL pointer");
+    const cudaError_t e = shared_error_word(word);
+    return e == cudaSuccess ? DFLASH_OK : cuda_fail(e, "address of the error word");
 }
 
 size_t dflash_logprobs_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t top_k)

@@ -21,6 +21,8 @@
 namespace dflash {
 namespace {
 
+__device__ __align__(256) uint32_t g_error_block[(256 + DFLASH_COUNTER_BYTES) / sizeof(uint32_t)];
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
@@ -207,6 +209,14 @@ static cudaError_t launch_join(const TreeAttnParams& p, cudaStream_t stream)
     cfg.numAttrs = 1;
     return share > 1 ? cudaLaunchKernelEx(&cfg, tree_join_kernel<V, true>, p, share)
                      : cudaLaunchKernelEx(&cfg, tree_join_kernel<V, false>, p, share);
+}
+
+cudaError_t shared_error_word(uint32_t** word)
+{
+    void* at = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&at, g_error_block);
+    if (e == cudaSuccess) *word = static_cast<uint32_t*>(at);
+    return e;
 }
 
 cudaError_t launch_tree_join(const TreeAttnParams& p, cudaStream_t stream)

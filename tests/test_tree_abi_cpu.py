@@ -206,3 +206,21 @@ def test_one_stride_of_rows():
         B._row_stride(x[:, :5], 20, 10)
     with pytest.raises(ValueError):
         B._row_stride(x.transpose(1, 2), 40, 6)
+
+
+@cpu_only
+@pytest.mark.parametrize("kw,code", [
+    (dict(err=FAKE + 2), B.ERR_INVALID_ARG), (dict(err=FAKE, ws=None), B.ERR_WORKSPACE),
+    (dict(err=FAKE, ws_bytes=300), B.ERR_WORKSPACE), (dict(err=None, ws=FAKE + 16), B.ERR_WORKSPACE),
+    (dict(err=FAKE, q=None), B.ERR_INVALID_ARG),
+])
+def test_tree_attn_with_a_word_refuses(lib, kw, code):
+    q, err, ws, ws_bytes = (kw.get(k, v) for k, v in (("q", FAKE), ("err", FAKE), ("ws", FAKE), ("ws_bytes", 1 << 40)))
+    assert lib.dflash_tree_attn_err(q, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, ctypes.byref(dims()), 4, 0, 0.1, 2 * FAKE, FAKE,
+                                    0, err, ws, ws_bytes, 0, 0) == code
+    assert lib.dflash_last_error_message()
+
+
+def test_shared_error_word_refuses_null(lib):
+    assert lib.dflash_shared_error_word(None) == B.ERR_INVALID_ARG
+    assert lib.dflash_last_error_message()

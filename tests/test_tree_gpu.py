@@ -1132,3 +1132,103 @@ def test_rows_of_scores_that_are_not_finite_come_out_as_nan(kernel, dtype, kind,
     same[node, head] = False
     assert torch.equal(out[same], want[same]) and torch.equal(lse[same], want_lse[same])
     assert torch.isfinite(out[same].float()).all() and torch.isfinite(lse[same]).all()
+
+
+# ------------------------------------------------------------------------ the word of device errors
+
+
+def on_device(t):
+    return (torch.from_numpy(t.table).cuda(), torch.tensor(t.lens, dtype=torch.int32, device="cuda"),
+            torch.from_numpy(t.parents).cuda(), torch.tensor(t.nodes, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("kernel,dtype", BOTH)
+def test_an_error_outlives_a_larger_call(kernel, dtype):
+    # the second call on the stream needs a larger workspace than the first
+    small, large = Tree([2], [30], dtype=dtype, seed=61), Tree([64], [5000], hq=32, hkv=4, d=512, dtype=dtype, seed=62)
+    small.table[0, 1] = small.k.shape[0]
+    stream = torch.cuda.Stream()
+    for t in (small, large):
+        args = on_device(t)
+        torch.cuda.synchronize()
+        dfl.tree_attn(t.q, t.k, t.v, *args[:3], num_nodes=args[3], kernel=kernel, stream=stream)
+    other = torch.cuda.Stream()
+    assert dfl.tree_attn_error(stream=other) == 0  # another stream's calls were sound
+    assert dfl.tree_attn_error(stream=stream, clear=False) == B.DEVERR_PAGE_ID
+    assert dfl.tree_attn_error(stream=stream) == B.DEVERR_PAGE_ID
+    assert dfl.tree_attn_error(stream=stream) == 0
+
+
+@pytest.mark.parametrize("kernel,dtype", BOTH)
+def test_errors_of_captured_calls_are_reported(kernel, dtype):
+    # two layers in a graph, which other graphs' and eager calls run between
+    t = Tree([6, 3], [100, 200], dtype=dtype, seed=63)
+    args = on_device(t)
+    o, l = torch.zeros_like(t.q), torch.zeros(t.q.shape[:2], device="cuda")
+
+    def layer(q, out):
+        return dfl.tree_attn(q, t.k, t.v, *args[:3], num_nodes=args[3], kernel=kernel, out=out, lse=l)
+
+    mid = torch.zeros_like(o)
+    layer(t.q, mid)
+    layer(mid, o)
+    torch.cuda.synchronize()
+    want = o.clone()
+    assert dfl.tree_attn_error() == 0
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer(t.q, mid)
+            layer(mid, o)
+        graphs.append(g)
+    good = args[0].clone()
+    for g in graphs:
+        g.replay()
+        assert dfl.tree_attn_error() == 0 and torch.equal(o, want)
+        args[0][1, 2] = -4
+        g.replay()
+        args[0].copy_(good)
+        graphs[0].replay()
+        graphs[1].replay()
+        layer(t.q, mid)
+        assert dfl.tree_attn_error(clear=False) == B.DEVERR_PAGE_ID
+        assert dfl.tree_attn_error() == B.DEVERR_PAGE_ID
+        assert dfl.tree_attn_error() == 0
+        g.replay()
+        assert dfl.tree_attn_error() == 0 and torch.equal(o, want)
+
+
+@pytest.mark.parametrize("kernel,dtype", BOTH)
+def test_a_given_word_takes_the_errors(kernel, dtype):
+    t = Tree([6, 3], [100, 200], T=6, dtype=dtype, seed=64)
+    args = on_device(t)
+    word, ws = torch.zeros(1, dtype=torch.int32, device="cuda"), None
+
+    def call(**kw):
+        return dfl.tree_attn(t.q, t.k, t.v, *args[:3], num_nodes=args[3], kernel=kernel, device_error=word, **kw)
+
+    out, lse = call()
+    assert word.item() == 0 and dfl.tree_attn_error() == 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    args[1][0] = 5
+    call()
+    assert word.item() == B.DEVERR_SEQ_LEN and dfl.tree_attn_error() == 0
+    args[2][1, 2] = 2  # (bits add up)
+    g.replay()
+    torch.cuda.synchronize()
+    assert word.item() == B.DEVERR_SEQ_LEN | B.DEVERR_TREE and dfl.tree_attn_error() == 0
+    # beside a given workspace: its own word stays as it is, whatever it holds
+    dims = dfl.make_dims(t.q, t.k, torch.from_numpy(t.table), 6)
+    ws = torch.full((dfl.tree_attn_workspace_bytes(dims, 6),), 255, dtype=torch.uint8, device="cuda")
+    word.zero_()
+    args[1][0], args[2][1, 2] = 100, 0
+    args[0][0, 0] = t.k.shape[0]
+    call(workspace=ws)
+    assert word.item() == B.DEVERR_PAGE_ID and (ws[:256] == 255).all()
+    for bad in (torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"),
+                torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            dfl.tree_attn(t.q, t.k, t.v, *args[:3], num_nodes=args[3], device_error=bad)

@@ -449,7 +449,8 @@ DFLASH_API dflash_status dflash_selector_walk(const void* pred_codebook, const v
  *   entropy = -sum_v exp(logp(v)) logp(v)        (a term of probability 0 is 0)
  *   top     = the top_k tokens of largest l_v, largest first, of equal ones the smaller id first
  * One pass over the logits: the running maximum, the sum of exponentials and the entropy's sum in
- * fp32, the top tokens selected exactly. A logit of -inf rules its token out: logp = -inf and
+ * fp32 (where the tokens beside the likeliest share a mass p below 2^-24, its logp and the entropy
+ * are off by up to p), the top tokens selected exactly. A logit of -inf rules its token out: logp = -inf and
  * no share in the sums. A row of nothing but -inf has log_z = -inf, every logp = -inf and
  * entropy 0. Logits must not be NaN or +inf (the row's results are then unspecified).
  * The top tokens and log probabilities have the form of dflash_selector_walk's candidates and unary.

@@ -3,8 +3,10 @@
 //   m = max_v l_v, y_v = (l_v - m) log2(e) / temperature, s = sum_v 2^y_v, w = sum_v y_v 2^y_v
 //   log_z = m / temperature + ln s,  logp(v) = (l_v - m) / temperature - ln s,  entropy = ln s - ln 2 * w / s
 // Sums are taken about the running maximum, which is subtracted from the logit itself before the scaling: the
-// differences stay exact to fp32 whatever the size of the logits, and a row with one likely token keeps its
-// small entropy.
+// differences stay exact to fp32 whatever the size of the logits. In a row with one likely token s is 1, the
+// maximum's own term, and the mass p of all the others: each of these is added to it once, off by at most what is
+// added (and by 2^-24), so that ln s loses p at most, where p is below 2^-24 all of it. The top token's logp is 0 then,
+// and the entropy p (1 - ln p) is p low, a twentieth of it: w, without a term of the maximum's, is exact to fp32.
 //
 // A row is cut into equal slices, a CTA of 128 threads each, streamed in steps of 16 values a thread with the
 // next step's loads in flight; no barrier until its end. Beside the sums a thread keeps the maximum of each

@@ -1232,3 +1232,38 @@ def test_a_given_word_takes_the_errors(kernel, dtype):
                 torch.zeros(1, dtype=torch.int32)):
         with pytest.raises(ValueError):
             dfl.tree_attn(t.q, t.k, t.v, *args[:3], num_nodes=args[3], device_error=bad)
+
+
+# ------------------------------------------------------------------ rows with one likely token
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [1000, 5000, 70001])
+@pytest.mark.parametrize("lead", [10.0, 16.0, 25.0, 30.0, 50.0])
+def test_logprobs_of_one_likely_token(dtype, V, lead):
+    # The others share a mass p / (1 + p) with p = sum exp(x - lead). Their terms are added up among themselves and to
+    # the 1 of the likely one once each; such an addition rounds by half a step of [1, 2), 2^-24, at most, and
+    # by no more than what it adds, as leaving 1 out of it would. So ln s is off by p, or by 2^-24 an addition: 8 in
+    # a thread's step, one per later step (at most 1 + V / 2048 / slices: a row alone has one), 9 in the CTA's join,
+    # V / 2048 / 128 + 1 + 9 in the slices': below 32. The entropy's other part, sum p y, is off by 2^-16 of itself: terms of
+    # |y| <= 80 with two roundings of the exponent (2^-17.2) and one of 2^-22, sums of few roundings.
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randint(-32, 1, (4, V), generator=g, device="cuda").float() / 8
+    at = torch.tensor([0, 7, V // 2, V - 1], device="cuda")
+    x[torch.arange(4, device="cuda"), at] = lead
+    x = x.to(dtype)
+    tokens = at.int()[:, None].contiguous()
+    given, ent, z, top, lp = dfl.token_logprobs(x, tokens, top_k=2)
+    wide = x.double()
+    e = (wide - lead).exp()
+    e[torch.arange(4, device="cuda"), at] = 0.0
+    p = e.sum(1)
+    y = (e * (wide - lead)).sum(1)
+    ln_s = torch.log1p(p)
+    lost = torch.minimum(p, torch.full_like(p, 32 * 2.0 ** -24))
+    want = ln_s - y / (1 + p)
+    assert ((ent.double() - want).abs() <= lost * (1 + 2.0 ** -16) + 2.0 ** -16 * want).all()
+    assert ((given[:, 0].double() + ln_s).abs() <= lost * (1 + 2.0 ** -16) + 2.0 ** -20 * ln_s).all()
+    assert torch.equal(top[:, 0], tokens[:, 0]) and torch.equal(lp[:, 0], given[:, 0])
+    # lead / 1 + ln s, rounded once more to half a step of 64
+    assert ((z.double() - lead - ln_s).abs() <= lost * (1 + 2.0 ** -16) + 2.0 ** -18).all()

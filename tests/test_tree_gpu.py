@@ -1267,3 +1267,19 @@ def test_logprobs_of_one_likely_token(dtype, V, lead):
     assert torch.equal(top[:, 0], tokens[:, 0]) and torch.equal(lp[:, 0], given[:, 0])
     # lead / 1 + ln s, rounded once more to half a step of 64
     assert ((z.double() - lead - ln_s).abs() <= lost * (1 + 2.0 ** -16) + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("kernel,dtype", BOTH)
+@pytest.mark.parametrize("hkv,d", [(1, 16), (1, 128), (2, 64)])
+def test_a_cache_of_one_page_and_requests_of_one_key(kernel, dtype, hkv, d):
+    # the page stride is never taken then, nor the head stride of one head
+    t = Tree([3], [13], hq=2 * hkv, hkv=hkv, d=d, dtype=dtype, page=16, seed=65)
+    only = int(t.table[0, 0])
+    t.k, t.v = (c[only:only + 1].clone() for c in (t.k, t.v))
+    t.table[0, 0] = 0
+    t.check(*t.call(kernel))
+    t.k, t.v = (c.as_strided(c.shape, (0,) + c.stride()[1:]) for c in (t.k, t.v))
+    t.check(*t.call(kernel))
+    t = Tree([1, 1, 0, 1], [1, 1, 0, 2], hq=2 * hkv, hkv=hkv, d=d, dtype=dtype, seed=66)
+    t.check(*t.call(kernel))
+    assert t.error() == 0

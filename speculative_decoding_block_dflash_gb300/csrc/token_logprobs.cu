@@ -19,12 +19,19 @@
 // ranked against each other (a key's rank is the number of larger ones; no sort) and the first k stay. The
 // buffer holds 256 candidates of each warp; a warp that might add more waits for a merge, so nothing but the
 // time depends on the data: a row of equal logits reads every group again. A thread's values of a step are
-// whole sectors, so that reading a group again fetches little beside it. Measured, k = 64 beside none: 1000
-// rows of 151937 fp32 129 and 107 us (floor 90), bf16 82 and 67 (45); 4000 rows of 32000 bf16 100 and 61 (38);
-// 8 rows of 151936 bf16 22 and 10. (Candidates picked step by step, with a sort of 256 per merge, took 460 us
-// for the first, with merges by rank at every doubling of what has been seen 143, with 16 groups a thread in
-// place of 32 137. A bound from all four warps alone, and a short last slice, took 43 us for the 8 rows: a warp
-// without values left no bound.)
+// whole sectors, so that reading a group again fetches little beside it.
+//
+// Measured in replayed graphs on inputs beyond L2, k = 64 beside none: 1000 rows of 151937 fp32 117 and 95 us
+// (floor 90), of 151936 bf16 76 and 61 (45); 4000 rows of 32000 bf16 93 and 57 (38); 8 rows of 151936 bf16 18 and
+// 6; 1 row fp32 16. Bound: fp32 the stream, then the groups read again, with no loads of the row ahead meanwhile;
+// bf16 the issue slots: a value costs what it costs in fp32, whose kernel issues in 54 us of its time for the first
+// of these sizes, which 45 us of stream do not hide. Rows a little above whole waves of CTAs (eight an SM) leave
+// the last wave mostly idle: 1216 rows of 151936 bf16 without top tokens 67 us, 1230 rows 101.
+//
+// (Earlier forms, timed call by call after a flush of L2, where this one took 117 us for the first size: candidates
+// picked step by step, with a sort of 256 per merge, 460; merges by rank at every doubling of what has been seen
+// 143; 16 groups a thread in place of 32 137. A bound from all four warps alone, and a short last slice, took 43 us for
+// the 8 rows in place of 27: a warp without values left no bound.)
 //
 // Slices leave their sums and keys in the workspace; the last CTA of a row to arrive (a counter, no waiting)
 // merges them the same way and writes the row.
@@ -40,7 +47,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kElems = 16;      // values per thread and step
 constexpr int kCtasPerSm = 8;
-constexpr int kSliceElems = 2048;  // a step: the shortest slice
+constexpr int kSliceElems = kElems * kThreads;  // a step
 constexpr int kMaxK = DFLASH_MAX_TOP_K;
 constexpr int kWarpRoom = 256;  // candidates a warp may add between merges: 32 vectors of bf16 at least
 constexpr int kCand = kThreads / 32 * kWarpRoom + 512;  // what may wait, and what may come before it is looked at
@@ -634,7 +641,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
 
 int32_t logprobs_slices(int32_t R, int32_t V)
 {
-    // one wave of CTAs, slices of kSliceElems logits or more; a slice more costs a row some microseconds of merging
+    // One wave of CTAs, but no more than a slice per step of the row: short rows are cut into slices of one step, half
+    // a step to a whole one each. A slice more costs a row some microseconds of merging.
     const int64_t wave = (int64_t)kCtasPerSm * device_sm_count();
     return (int32_t)std::max<int64_t>(1, std::min<int64_t>(wave / R, ((int64_t)V + kSliceElems - 1) / kSliceElems));
 }

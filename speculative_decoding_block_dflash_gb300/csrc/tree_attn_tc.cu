@@ -40,12 +40,12 @@
 // its id is read one stage ahead by the lane that issues it. Boxes past the keys or before the window are
 // fetched at an out-of-bounds page, which the TMA unit fills with zeros without a look at the table.
 //
-// Bounds and what was measured (calls back to back): long contexts the K/V stream, 4 requests of 120k to 128k keys, 32
-// nodes, 32/8 heads of 128: 331 us, 6.2 TB/s. Many rows per key the chain MMA - softmax - MMA, 8 ragged requests of
-// up to 32k keys, 64 nodes: 134 us, 0.95 PFLOP/s (0.85 us a pair tile, of which the MMAs are some 0.65). Short calls
-// the start (lengths, page table, first K: 6 us), the bytes an SM takes in (some 44 GB/s of the whole rate each) and
-// the join: one request of 8192 keys, 24 nodes, 32/4 heads of 512: 33 us; 4 sliding windows of 1024, 16 nodes, 32/16
-// heads of 256: 28 us.
+// Bounds and what was measured (calls back to back, ranges over several GPUs): long contexts the K/V stream, 4
+// requests of 120k to 128k keys, 32 nodes, 32/8 heads of 128: 324 to 342 us, 6.0 to 6.35 TB/s. Many rows per key
+// the chain MMA - softmax - MMA, 8 ragged requests of up to 32k keys, 64 nodes: 133 to 138 us, 0.93 to 0.96 PFLOP/s
+// (0.85 us a pair tile, of which the MMAs are some 0.65). Short calls the start (lengths, page table, first K: 6 us),
+// the bytes an SM takes in (some 44 GB/s of the whole rate each) and the join: one request of 8192 keys, 24 nodes,
+// 32/4 heads of 512: 33 us; 4 sliding windows of 1024, 16 nodes, 32/16 heads of 256: 28 us.
 //
 // Every mbarrier wait is bounded (p.wait_ns): on expiry the kernel records DFLASH_DEVERR_TIMEOUT, waits
 // (bounded) for its own copies and MMAs, frees TMEM and returns.
@@ -802,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float tot = ms.l[0][row] + ms.l[1][row];
             const float inv = tree_inv_sum(tot, whole);
             if (live_row && half == 0) {
+                // (the sum of a row is 1 or more: __log2f is off by 2^-22 up to 2, by 2 ulp of the logarithm above)
                 const float lse = tree_row_lse((m2 + __log2f(tot)) * kLn2, tot, whole);
                 if (!whole)
                     p.part_lse[prow] = lse;

@@ -8,8 +8,8 @@
 //
 // The request's positions and page offsets are worked out once per CTA into shared memory. Bound: latency
 // (few bytes; the load and the store are two trips to memory, after two for the path and the pages).
-// Measured: 4 moves in one layer (4 heads of 512) 3.0 us a call in a graph; 32 requests' 6 moves in 32 layers (8 heads
-// of 128, 27 MB) 6.9 us.
+// Measured in replayed graphs: 4 moves in one layer (4 heads of 512) 2.9 us; 32 requests' 6 moves in 32 layers (8 heads
+// of 128, 27 MB) 6.3 us where L2 holds the slots, 9.5 where it does not.
 #include <algorithm>
 
 #include "dflash_device.cuh"

@@ -1,18 +1,20 @@
 // Join of the tree attention's partials: a (request, KV head) pair whose key tiles lie in several
 // ranges has one normalised partial (o_c, lse_c) per range and row, and
 //   m = max_c lse_c, w_c = exp(lse_c - m), out = sum_c w_c o_c / sum_c w_c, lse = m + log(sum_c w_c).
-// A partial of scores that are not finite has a NaN lse; the maximum hands it on, so that the row is NaN as a whole pair's
-// would be.
-// Pairs that one range holds whole are final already. A request with a bad length or tree size gets its
-// zeros here.
+// A partial of scores that are not finite has a NaN lse; the maximum hands it on, so that the row is NaN as a whole
+// pair's would be. Pairs that one range holds whole are final already. A request with a bad length or tree size gets
+// its zeros here.
 //
 // A warp takes a row, or where there are few rows 2, 4 or 8 warps take one, a stretch of its partials each, and add
 // theirs up in shared memory, in order. A warp's lanes read the partials' lse values (32 at a time) and form the weights
 // while the first partial rows come, four to sixteen a time. Launched as a programmatic dependent of the attention
 // kernel; the deal of tiles to ranges is worked out before the wait for it. Bound: trips to L2, two to start with and
-// one more per batch of partials; behind the attention it adds 3 to 7 us. Measured, whole calls of one request: 1 node,
-// 16/1 heads of 128, 100k keys (151 partials a row) 33 us, 51 with a warp per row; 7 nodes, 12/2 heads of 96, 18k keys
-// 22.5, 41 with a warp per row.
+// one more per batch of partials; behind the attention it adds 3 to 7 us. Measured, whole calls of one request after a
+// flush of L2: 1 node, 16/1 heads of 128, 100k keys (151 partials a row) 33 us, 51 with a warp per row; 7 nodes, 12/2
+// heads of 96, 18k keys 22.5, 41 with a warp per row (back to back on inputs beyond L2 25 and 17 now).
+//
+// Every CTA walks all requests twice, 32 a step, to find its ranges, so that the time of large batches grows with
+// their square: 4 nodes, 200 to 300 keys, 32/8 heads of 128, 256 requests 127 us, 1024 573, 4096 4660.
 #include <algorithm>
 #include <cmath>
 

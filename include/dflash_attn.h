@@ -697,14 +697,16 @@ DFLASH_API dflash_status dflash_append_kv(const void* k, const void* v, int32_t 
  *   parents given    a drafted tree: dflash_tree_attn's mask (causal must be 0)
  * s, out and lse are those of dflash_block_attn. On the CUDA cores scores are of q as it is, all in fp32. On the tensor
  * cores q is held as a sum of two e4m3 numbers, off by at most 2^-17 of the largest |q| of its row, and a probability times its
- * page's v_scale by at most 2^-9 of itself (as bf16 would be), or 2^-26 of the largest such product of its row; sums are fp32.
+ * page's v_scale by at most 2^-9 of itself (as bf16 would be), or 2^-26 of the largest such product of its row; sums are fp32,
+ * and a key whose weight is below 2^-62 of its row's largest may be missing from them.
  *
  *   q             device, [B*T, Hq, D] contiguous, dims->dtype; padding rows may hold anything. A row of q that is not
  *                 finite, or a score that is not, makes the row NaN with a NaN lse; other rows are not touched by it.
  *   k_cache, v_cache  device, e4m3 bytes, the layout of dflash_block_attn (strides in bytes, multiples of 16). Keys
  *                 outside [first visible, L_b) are never used, whatever they hold. The visible keys' K and V are finite.
- *   k_scale, v_scale  device float32 [num_pages, num_kv_heads], finite and >= 0. The tensor cores take a v_scale below
- *                 2^-90 (0, a page of zeros) as 2^-90 and one above 2^90 as 2^90.
+ *   k_scale, v_scale  device float32 [num_pages, num_kv_heads], finite and >= 0. The tensor cores take a v_scale of up to
+ *                 2^-126 (a page of zeros) as 2^-40. Where a visible page has another outside [2^-40, 2^24], that part of
+ *                 the request is worked out on the CUDA cores, at a small fraction of the speed.
  *   num_queries, parents  device int32 [B], [B, T], or NULL.
  *   causal        0 or 1; window 0 or W >= 1, in a non-causal block W >= T.
  *   kernel        as in dflash_tree_attn; TC takes bf16 q.

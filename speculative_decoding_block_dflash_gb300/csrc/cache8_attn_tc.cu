@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             named_bar_sync_256();  // O, the sums and the masks are read before the next piece's steps
         });
+        if (named_bar_or_256(ok && ms.far != 0)) far_pieces(p, x.page_magic, range, sub, ms.par, lo_s, anc_s);
     } else {
         give_registers();
         if (warp == kKWarp) {

@@ -16,7 +16,13 @@
 // what counts is then some 2^-18 of it each), hence fp16, or three e5m2 numbers. The value scale of a page goes into the exponent,
 //   P' = 2^(x + log2 vs - m'), m' the lazy maximum of x + log2 vs,
 // so that P' is rounded relative to the largest p vs of its row, whatever the scales are; the row sum adds P' / vs in fp32.
-// Scales count as within [2^-90, 2^90], which keeps the sums in fp32's range.
+//
+// P' is 0 below 2^-126, and then so is P' / vs, where its key's weight need not be small. So that holds for scales within
+// [2^-40, 2^24], among which no weight above 2^-62 of its row's largest is lost. Scales up to 2^-126, those of pages of zeros,
+// count as 2^-40. A piece with any other scale is worked out once more on the CUDA cores when the CTA is done with all of its
+// pieces, from q, K and V as they are (far_pieces): the loops above know nothing of it. (A second sum of weights in them, which some
+// five forms of cost chunks of 256 queries 3 to 14 % and blocks with a window 2 to 11 % without ever being formed: their code is
+// fetched every time, and their registers are all in use. This costs at most 0.6 us.)
 #pragma once
 
 #include <cuda.h>
@@ -40,6 +46,7 @@ constexpr int kGroups = kTile / kGroup;
 constexpr int kStageBytes = 16384;
 constexpr int kMaxStages = 8;  // of each ring
 constexpr int kScaleRing = 8;  // tiles
+constexpr float kNearLow = -40.f, kNearHigh = 24.f;  // logarithms of the value scales that P' and the row sums take
 constexpr int kConverters = 4;
 // warps behind the 8 of the softmax
 constexpr int kKWarp = 8;
@@ -91,6 +98,7 @@ struct Pipe {
     int32_t par[DFLASH_MAX_TREE_NODES];
     int32_t pieces, more;
     Piece piece[kPieces];
+    int32_t far;  // a piece had a value scale too far from 1
 };
 
 // Bounded wait, of little code: false when it ran out (recorded) or another warp has given up. The test suspends the warp, so
@@ -179,6 +187,7 @@ __device__ __forceinline__ void init_pipe(Pipe& ms, int r_empty_count, int p_hal
     }
     mbar_init(&ms.drain, 1);
     ms.abort = 0;
+    ms.far = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
@@ -226,6 +235,12 @@ __device__ __forceinline__ int32_t page_id(const TreeAttnParams& p, const Shape&
     const int32_t pg = (int32_t)(x.page_magic ? __umulhi(group, x.page_magic) : group);
     slot = key - pg * p.page_size;
     return __ldg(p.page_table + (int64_t)b * p.max_pages + pg);
+}
+
+// Whether a value scale is one that P' does not take.
+__device__ __forceinline__ bool is_far(float v_scale)
+{
+    return v_scale > 0x1p-126f && !(v_scale >= 0x1p-40f && v_scale <= 0x1p24f);
 }
 
 // A producer warp: K or V by TMA. Boxes without a visible key are fetched at an out-of-bounds page, which the TMA unit fills
@@ -328,7 +343,8 @@ __device__ __forceinline__ void fetch_scales(const TreeAttnParams& p, const Shap
             float next_ks, next_vs;
             scales_of(next_page, next_ks, next_vs);
             next_page = group_page(t + 2);
-            const float v_log = fminf(fmaxf(log2f(vs), -90.f), 90.f);
+            if (is_far(vs)) ms.far = 1;
+            const float v_log = fminf(fmaxf(log2f(vs), kNearLow), kNearHigh);
             ok = wait(ms.sc_free + pos.idx, pos.phase ^ 1u);
             if (!ok) break;
             if (lane < kGroups) {
@@ -515,6 +531,149 @@ __device__ __forceinline__ void convert(const TreeAttnParams& p, const Shape& x,
             }
         }
     });
+}
+
+// The pieces of a range with a value scale that is far from 1, on the CUDA cores in fp32, in place of what the tensor cores have left
+// there: a warp per row, 8 keys a step, a running maximum of the scores and the sum of the weights beside it. Called by the 8
+// warps of the softmax when all pieces are done; each walks them by itself, as another role may still look at the table.
+static __device__ __noinline__ void far_pieces(const TreeAttnParams& p, uint32_t page_magic, int32_t range, int32_t sub,
+                                               int32_t* par_s, int32_t* lo_s, uint32_t* anc_s)
+{
+    constexpr int kWords = DFLASH_MAX_HEAD_DIM / 128;  // of four dims, a lane's
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const SubTile st = sub_tile(p, sub);
+    const int32_t node0 = st.rt * p.npt, words = (p.T + 31) / 32;
+    const float scale = p.scale * kLog2e;
+    Shape x{};
+    x.page_magic = page_magic;
+    PieceWalk w;
+    w.start(p, range);
+#pragma unroll 1
+    for (; !w.done(); w.next(p)) {
+        const TreeReq req = w.req;
+        if (req.n <= node0) continue;
+        const int32_t first = (req.tile0 + w.t0) * kTile, end = min(req.L, (req.tile0 + w.t1) * kTile);
+        // the pages that some query sees, as the scale warp takes them
+        bool far = false;
+#pragma unroll 1
+        for (int32_t key = first + lane * kGroup; key < end; key += 32 * kGroup) {
+            if (key + kGroup <= req.lo) continue;
+            int32_t slot;
+            const int32_t page = page_id(p, x, w.b, key, slot);
+            if (page >= 0 && page < p.num_pages) far |= is_far(__ldg(p.v_scale + (int64_t)page * p.Hkv + w.g));
+        }
+        if (!__any_sync(0xffffffffu, far)) continue;  // (the same for all warps)
+        named_bar_sync_256();
+        tree_load_parents(p, w.b, req.n, par_s, tid, 256);
+        named_bar_sync_256();
+        tree_walk_nodes(p, req, node0, min(p.npt, req.n - node0), par_s, anc_s, lo_s, tid, 256);
+        named_bar_sync_256();
+        const int32_t live = min(p.npt, req.n - node0) * p.Gc;
+        const bool whole = w.whole();
+        const int64_t prow = tree_part_row(p, range, sub, w.slot());
+#pragma unroll 1
+        for (int32_t row = warp; row < live; row += 8) {
+            const int32_t nd = row / p.Gc;
+            const int64_t orow =
+                ((int64_t)w.b * p.T + node0 + nd) * p.Hq + w.g * p.G + st.gc * p.Gc + (row - nd * p.Gc);
+            const uint32_t* anc = anc_s + nd * words;
+            const int32_t lo = lo_s[nd];
+            float q[kWords][4], acc[kWords][4];
+#pragma unroll
+            for (int c = 0; c < kWords; ++c) {
+                const int32_t d = c * 128 + lane * 4;
+                const uint2 v = d < p.D ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + orow * p.D + d))
+                                        : make_uint2(0, 0);
+                q[c][0] = u2f(v.x << 16), q[c][1] = u2f(v.x & 0xFFFF0000u);
+                q[c][2] = u2f(v.y << 16), q[c][3] = u2f(v.y & 0xFFFF0000u);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[c][u] = 0.f;
+            }
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int32_t key0 = first; key0 < end; key0 += kGroup) {
+                uint32_t seen = 0;  // the group's keys that the row sees
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    const int32_t key = key0 + k, a = key - req.ctx;
+                    const bool on = key < end && (a < 0 ? key >= lo : ((anc[a >> 5] >> (a & 31)) & 1u) != 0);
+                    seen |= (uint32_t)on << k;
+                }
+                if (!seen) continue;
+                int32_t slot;
+                const int32_t page = page_id(p, x, w.b, key0, slot);
+                const bool good = page >= 0 && page < p.num_pages;  // (else its keys read as zeros, and the error is raised)
+                const int64_t scale_at = (int64_t)page * p.Hkv + w.g;
+                const float ks = good ? __ldg(p.k_scale + scale_at) : 0.f, vs = good ? __ldg(p.v_scale + scale_at) : 0.f;
+                const int64_t at = (int64_t)page * p.sp + (int64_t)slot * p.ss + (int64_t)w.g * p.sh;
+                uint32_t e4[kGroup][kWords];
+                auto load = [&](const void* base) {
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+                        for (int c = 0; c < kWords; ++c) {
+                            const int32_t d = c * 128 + lane * 4;
+                            e4[k][c] = 0u;
+                            if (good && ((seen >> k) & 1u) && d < p.D)
+                                e4[k][c] =
+                                    __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + at + k * p.ss + d));
+                        }
+                };
+                load(p.k);
+                float y[kGroup], top = m;
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    y[k] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kWords; ++c) {
+                        float f[4];
+                        e4m3_values(e4[k][c], f);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) y[k] = fmaf(q[c][u], f[u] * ks, y[k]);
+                    }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) y[k] += __shfl_xor_sync(0xffffffffu, y[k], off);
+                    y[k] *= scale;
+                    if ((seen >> k) & 1u) top = fmaxf(top, y[k]);
+                }
+                load(p.v);
+                const float alpha = top > m ? ex2(m - top) : 1.f;  // 0 from -inf
+                m = top;
+                l *= alpha;
+#pragma unroll
+                for (int c = 0; c < kWords; ++c)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[c][u] *= alpha;
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    const float e = (seen >> k) & 1u ? ex2(y[k] - m) : 0.f;
+                    l += e;
+#pragma unroll
+                    for (int c = 0; c < kWords; ++c) {
+                        float f[4];
+                        e4m3_values(e4[k][c], f);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) acc[c][u] = fmaf(e, f[u] * vs, acc[c][u]);
+                    }
+                }
+            }
+            const float inv = tree_inv_sum(l, whole), lse = tree_row_lse((m + log2f(l)) * kLn2, l, whole);
+            if (lane == 0 && !whole) p.part_lse[prow + row] = lse;
+            if (lane == 0 && whole && p.lse) p.lse[orow] = lse;
+#pragma unroll
+            for (int c = 0; c < kWords; ++c) {
+                const int32_t d = c * 128 + lane * 4;
+                if (d >= p.D) continue;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (!whole)
+                        p.part_out[(prow + row) * p.DV + d + u] = acc[c][u] * inv;
+                    else
+                        static_cast<__nv_bfloat16*>(p.out)[orow * p.D + d + u] = __float2bfloat16_rn(acc[c][u] * inv);
+                }
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------------------------------- host side

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         seen |= (uint64_t)vis << q;
                     }
                 }
-                // The scores of group g of this key: (S as it is) times the key's scale times the rows' c, plus `add`
+                // The scores of group g of this key: S times (the key's scale times the rows' c), plus log2 vs and `shift`
                 const uint64_t ks2 = pack2(ks, ks), log2v = pack2(v_log, v_log);
                 auto scaled = [&](const uint32_t (&r)[8], const uint32_t (&r2)[8], int g, uint32_t bits, const float* shift,
                                   float (&y)[8]) {
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int u = 0; u < 8; u += 2) {
                         uint64_t v = pack2(u2f(r[u]), u2f(r[u + 1]));
                         if (kStack) v = add2(v, pack2(u2f(r2[u]), u2f(r2[u + 1])));
-                        v = fma2(mul2(v, ks2), pack2(c[u], c[u + 1]), log2v);
+                        v = fma2(v, mul2(pack2(c[u], c[u + 1]), ks2), log2v);  // (S times the key's scale may leave fp32's range)
                         if (shift) v = add2(v, pack2(sh[u], sh[u + 1]));
                         unpack2(v, y[u], y[u + 1]);
                     }

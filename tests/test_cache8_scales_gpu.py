@@ -184,3 +184,16 @@ def test_an_appended_infinity_has_one_meaning():
     assert t.scales[1][int(t.table[0][77 // 16]), 0] == 2.0 ** 120
     for kernel in KERNELS:
         check(t, *t.call(kernel), kernel)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("T,hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("power", [116, -110])
+def test_key_scales_that_undo_the_queries(T, hq, hkv, d, power, kernel):
+    """Tiny queries on keys of huge scales, and the other way round: ordinary scores."""
+    t = Attn([T], [max(T, 200)], T=T, hq=hq, hkv=hkv, d=d, seed=2)
+    t.q *= 2.0 ** -power
+    t.scales[0] *= 2.0 ** power
+    out, lse = t.call(kernel)
+    assert out.isfinite().all() and lse.isfinite().all()
+    check(t, out, lse, kernel)

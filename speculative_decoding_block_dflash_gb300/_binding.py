@@ -1048,11 +1048,15 @@ def make_rope(rotary_dim: int, base: float = 10000.0, layout: str = "half", scal
 
     layout "half" pairs dims i and i + rotary_dim / 2, "interleaved" 2i and 2i + 1. Scalings for contexts `factor` times
     as long: "linear" divides every f_i by it (position interpolation); "ntk" takes the base base * factor^(r / (r - 2)),
-    r = rotary_dim, which leaves the fastest pair as it is and divides the slowest by factor; "yarn" (Peng et al., YaRN,
-    2023) divides those that turn less than beta_slow times in original_len positions, keeps those that turn more than
-    beta_fast times, blends linearly between, and scales cosine and sine by a gain of 0.1 ln(factor) + 1. inv_freq (numbers
-    or a tensor of rotary_dim / 2) gives the f_i instead, gain another factor of cosine and sine. The table is made on
-    the host, exactly from 64-bit floats."""
+    r = rotary_dim, which leaves the fastest pair as it is and divides the slowest by factor. "yarn" and "yarn_index" (Peng et
+    al., YaRN, 2023) divide the pairs that turn less than beta_slow times in original_len positions, keep those that turn more
+    than beta_fast times, blend linearly between, and scale cosine and sine by a gain of 0.1 ln(factor) + 1. They differ in what
+    the blend is linear in: in "yarn" the number of turns, as the paper's text defines it; in "yarn_index" the pair's index,
+    from the last pair of more than beta_fast turns to the first of less than beta_slow. Models published with such a scaling
+    are as a rule trained and served with the latter: take "yarn_index" for a checkpoint unless it says otherwise. (For base
+    10^4, 128 dims, factor 4 and 32768 positions 24 of the 64 frequencies differ, by up to 42 %.) inv_freq (numbers or a tensor
+    of rotary_dim / 2) gives the f_i instead, gain another factor of cosine and sine. The table is made on the host, exactly
+    from 64-bit floats."""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and >= 2")
     if inv_freq is not None:
@@ -1071,17 +1075,27 @@ def make_rope(rotary_dim: int, base: float = 10000.0, layout: str = "half", scal
         f = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
         if scaling == "linear":
             f = [x / factor for x in f]
-        elif scaling == "yarn":
+        elif scaling in ("yarn", "yarn_index"):
             if original_len < 1 or not beta_fast > beta_slow:
                 raise ValueError("'yarn' needs original_len >= 1 and beta_fast > beta_slow")
+            if scaling == "yarn_index":
+                if not (base > 1 and beta_slow > 0):
+                    raise ValueError("'yarn_index' needs base > 1 and beta_slow > 0")
+                # the index at which a pair makes so many turns, the blend's ends rounded outwards and kept within the head
+                first, last = (rotary_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))
+                               for turns in (beta_fast, beta_slow))
+                first, last = max(math.floor(first), 0), min(math.ceil(last), rotary_dim - 1)
             for i, x in enumerate(f):
-                keep = (original_len * x / (2 * math.pi) - beta_slow) / (beta_fast - beta_slow)
+                if scaling == "yarn":
+                    keep = (original_len * x / (2 * math.pi) - beta_slow) / (beta_fast - beta_slow)
+                else:
+                    keep = (last - i) / (last - first) if last > first else float(i <= first)
                 keep = min(1.0, max(0.0, keep))
                 f[i] = x / factor * (1 - keep) + x * keep
             if gain is None:
                 gain = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
         elif scaling not in ("none", "ntk"):
-            raise ValueError("scaling must be 'none', 'linear', 'ntk' or 'yarn'")
+            raise ValueError("scaling must be 'none', 'linear', 'ntk', 'yarn' or 'yarn_index'")
     if not all(math.isfinite(x) for x in f):
         raise ValueError("frequencies must be finite")
     turns = []

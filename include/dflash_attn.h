@@ -674,8 +674,8 @@ DFLASH_API dflash_status dflash_rope(const void* x, void* out, dflash_dtype dtyp
  *   page_table    device int32 [batch, max_pages]; seq_lens device int32 [batch].
  *   dims          as in dflash_block_attn; num_q_heads is checked and not used.
  *   device_error  device uint32 word (bits OR-ed in) or NULL.
- * A request with new rows whose L_b lies outside [n_b, max_seq_len], or whose rows end behind num_tokens, is left out
- * (DFLASH_DEVERR_SEQ_LEN); a page id outside [0, num_pages) sets DFLASH_DEVERR_PAGE_ID and its tokens are left out. Pages
+ * A request with new rows whose L_b lies outside [n_b, max_seq_len], or whose rows are not all among the num_tokens (starts
+ * below 0, rows that end or lie behind them), is left out (DFLASH_DEVERR_SEQ_LEN, as starts that decrease raise); a page id outside [0, num_pages) sets DFLASH_DEVERR_PAGE_ID and its tokens are left out. Pages
  * that take new tokens must belong to one request only and stand in its table once. Limits: 0 <= num_tokens <= 2^24 (0 is
  * a no-op). Invalid arguments are reported before any launch. Asynchronous on `stream`; needs no workspace.
  */

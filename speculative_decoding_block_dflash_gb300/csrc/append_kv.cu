@@ -74,6 +74,16 @@ __device__ __forceinline__ Owner owner_of(const AppendParams& p, int32_t r, bool
     return o;
 }
 
+// A CTA's look at the table of starts: requests whose new rows are not all among the inputs', some of which no row leads to.
+__device__ __forceinline__ void check_starts(const AppendParams& p)
+{
+    if (!p.starts || !p.err) return;
+    for (int32_t b = threadIdx.x; b < p.B; b += kThreads) {
+        const int32_t first = __ldg(p.starts + b), next = __ldg(p.starts + b + 1);
+        if (next < first || (next > first && (first < 0 || next > p.N))) raise_error(p.err, DFLASH_DEVERR_SEQ_LEN);
+    }
+}
+
 __device__ __forceinline__ int32_t page_of(const AppendParams& p, int32_t b, int32_t pos)
 {
     const int32_t id = __ldg(p.page_table + (int64_t)b * p.max_pages + pos / p.page_size);
@@ -88,6 +98,10 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) append_same_kernel(const AppendParams p, const RopeUnits g)
 {
     const bool value = blockIdx.y == 1;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (!value) check_starts(p);
+        return;
+    }
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int32_t units = value ? (p.D + 15) / 16 : g.units;
     const int64_t rest = id / units;
@@ -162,12 +176,16 @@ __device__ __forceinline__ uint4 reencoded(const uint4& w, float old, float inv)
     return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-// Grid: rows in windows of `window`, groups of 8 heads, K and V.
+// Grid: rows in windows of `window` and a CTA for the table of starts, groups of 8 heads, K and V.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, 2) append_e4m3_kernel(const AppendParams p, const RopeUnits gk, const int32_t window)
 {
     __shared__ CosSin table[kTable];
     const bool value = blockIdx.z == 1;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (!value && blockIdx.y == 0) check_starts(p);
+        return;
+    }
     const RopeUnits g = value ? rope_units(p.D, 0, 0) : gk;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t h = blockIdx.y * kWarps + warp;
@@ -345,9 +363,9 @@ cudaError_t launch_typed(const AppendParams& p, cudaStream_t stream)
 {
     const RopeUnits g = rope_units(p.D, p.half, p.interleaved);
     if (!p.k_scale) {
-        const int64_t threads = (int64_t)p.N * p.Hkv * std::max(g.units, (p.D + 15) / 16);
+        const int64_t threads = (int64_t)p.N * p.Hkv * std::max(g.units, (p.D + 15) / 16);  // (and a CTA for the table of starts)
         append_same_kernel<T, kVec>
-            <<<dim3((unsigned)((threads + kThreads - 1) / kThreads), 2), kThreads, 0, stream>>>(p, g);
+            <<<dim3((unsigned)((threads + kThreads - 1) / kThreads + 1), 2), kThreads, 0, stream>>>(p, g);
         return cudaGetLastError();
     }
     // A CTA looks for owners among `window` rows. One row where there are few rows, so that every page has a CTA of its own;
@@ -356,7 +374,7 @@ cudaError_t launch_typed(const AppendParams& p, cudaStream_t stream)
     const int64_t fair = (int64_t)p.N * groups * 2 / (4 * device_sm_count());
     const int32_t window = (int32_t)std::max<int64_t>(1, std::min<int64_t>(fair, std::min(p.page_size, 32)));
     append_e4m3_kernel<T, kVec>
-        <<<dim3((unsigned)((p.N + window - 1) / window), (unsigned)groups, 2), kThreads, 0, stream>>>(p, g, window);
+        <<<dim3((unsigned)((p.N + window - 1) / window + 1), (unsigned)groups, 2), kThreads, 0, stream>>>(p, g, window);
     return cudaGetLastError();
 }
 

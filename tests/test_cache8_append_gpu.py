@@ -1,0 +1,84 @@
+"""GPU checks of what an append reports and leaves alone."""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_block_dflash_gb300 as dfl
+from speculative_decoding_block_dflash_gb300 import _binding as B
+from speculative_decoding_block_dflash_gb300 import build as build_mod
+from test_cache8_gpu import Append, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build_mod.build()
+    dfl.load_library()
+
+
+def pages_of(a, b):
+    return [int(x) for x in a.table[b] if x >= 0]
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("starts,left_out", [
+    ([0, 4, 100, 104], (1, 2)),    # rows that end behind the inputs, and rows that lie behind them
+    ([0, 4, 8, 3000], (2,)),       # (lengths below suit 4 rows)
+    ([-4, 0, 4, 8], (0,)),         # wholly before them
+    ([-2, 2, 6, 10], (0,)),        # and in part
+    ([0, 4, 8, 2 ** 31 - 1], (2,)),
+])
+def test_starts_outside_the_inputs_are_reported(starts, left_out, e4m3):
+    a = Append([4, 4, 4], [10, 20, 10], e4m3=e4m3)
+    a.starts = starts
+    before = a.numpy()
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a.call(device_error=word)
+    assert word.item() == B.DEVERR_SEQ_LEN
+    got = a.numpy()
+    for b in range(3):
+        pages = pages_of(a, b)
+        same = [np.array_equal(x[pages], y[pages]) for x, y in zip(before[0], got[0])]
+        assert all(same) if b in left_out else not any(same), b
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_rows_behind_the_inputs_of_many_requests(e4m3):
+    """The last of 700 requests claims a row that is not there; nothing else is wrong."""
+    a = Append([1] * 700, [3] * 700, hkv=1, d=16, e4m3=e4m3)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a.call(device_error=word)
+    assert word.item() == 0
+    a = Append([1] * 700, [3] * 700, hkv=1, d=16, e4m3=e4m3)
+    a.k, a.v = a.k[:-1], a.v[:-1]
+    before = a.numpy()
+    a.call(device_error=word)
+    assert word.item() == B.DEVERR_SEQ_LEN
+    got = a.numpy()
+    assert all(np.array_equal(x[pages_of(a, 699)], y[pages_of(a, 699)]) for x, y in zip(before[0], got[0]))
+    assert not any(np.array_equal(x[pages_of(a, 698)], y[pages_of(a, 698)]) for x, y in zip(before[0], got[0]))
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_starts_that_decrease_are_reported(e4m3):
+    a = Append([4, 4], [10, 20], e4m3=e4m3)
+    a.starts = [4, 0, 8]
+    a.lens = [30, 30]
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a.table = np.where(a.table < 0, a.table.max(), a.table)
+    a.call(device_error=word)
+    assert word.item() & B.DEVERR_SEQ_LEN
+
+
+def test_starts_within_the_inputs_are_not_reported():
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for e4m3 in (True, False):
+        for pad in (0, 5):
+            a = Append([0, 4, 0, 7, 0], [0, 10, 3, 20, 9], e4m3=e4m3, pad=pad)
+            a.call(device_error=word)
+            assert word.item() == 0
+        a = Append([0, 4, 0], [0, 10, 3], e4m3=e4m3)
+        a.starts = [100, 100, 100, 100]  # nobody has new rows, wherever they would be
+        a.call(device_error=word)
+        assert word.item() == 0

@@ -652,7 +652,7 @@ DFLASH_API dflash_status dflash_rope(const void* x, void* out, dflash_dtype dtyp
  * Appends new keys and values to the paged cache, the keys rotated on the way. Request b's n_b new rows are rows
  * starts[b] .. starts[b+1] - 1 of k and v (starts == NULL: num_tokens / batch rows each) and go, in order, to positions
  * L_b - n_b .. L_b - 1 with L_b = seq_lens[b] (the new tokens counted). Rows before starts[0] or from starts[batch] on
- * are padding and not read. A row is rotated to its position in the cache, or to positions[row] where given (drafted
+ * are padding: what they hold does not matter, but all num_tokens rows of k and v must be readable. A row is rotated to its position in the cache, or to positions[row] where given (drafted
  * trees, whose nodes' positions are not their slots).
  *
  * Caches of dims->dtype (no scales): the rotated key in fp32, rounded once; values as they are.

@@ -904,9 +904,9 @@ def tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
 
 
 def tree_attn_error(device=None, stream=None, clear: bool = True) -> int:
-    """DEVERR_* bits of the tree_attn and cache8_attn calls without a device_error and a workspace: of the stream's, and
-    of the device's captured ones, whatever stream replays them (a replay on another stream has to be waited for first); synchronises
-    the stream."""
+    """DEVERR_* bits of the tree_attn and cache8_attn calls without a device_error and a workspace, and of the append_kv
+    calls without a device_error: of the stream's, and of the device's captured ones, whatever stream replays them (a replay
+    on another stream has to be waited for first); synchronises the stream."""
     dev = torch.device("cuda" if device is None else device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
@@ -1199,7 +1199,8 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     float8_e4m3fn with k_scale and v_scale float32 [num_pages, Hkv]; page_table int32 [B, max_pages]; seq_lens int32 [B],
     the new tokens counted. Request b's rows are starts[b] .. starts[b + 1] - 1 (int32 [B + 1]; None: N / B each), and go to
     the last positions of its seq_lens[b]. positions int32 [N]: what the keys are rotated to, if not to their place in the
-    cache. Caches and scales are written in place. device_error: an optional int32 device word that receives DEVERR_* bits."""
+    cache. Caches and scales are written in place. device_error: an int32 device word that receives DEVERR_* bits (tokens of
+    a bad length, table of starts or page id are left out); without one tree_attn_error() reads them."""
     lib = _lib or load_library()
     shape = k.shape
     if len(shape) != 3 or not k.is_cuda or v.shape != shape or v.dtype is not k.dtype:
@@ -1234,6 +1235,8 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     if ctx is not None:
         ctx.__enter__()
     try:
+        if word is None:
+            word = _tree_word(dev, handle)
         st = lib.dflash_append_kv(k.data_ptr(), v.data_ptr(), N, ks[0], ks[1], vs[0], vs[1], starts_at, pos_at, ref,
                                   k_cache.data_ptr(), v_cache.data_ptr(), k_scale_at, v_scale_at, table_at, lens_at,
                                   dims_ref, word, handle)

@@ -82,3 +82,44 @@ def test_starts_within_the_inputs_are_not_reported():
         a.starts = [100, 100, 100, 100]  # nobody has new rows, wherever they would be
         a.call(device_error=word)
         assert word.item() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_errors_of_calls_without_a_word_are_kept(e4m3):
+    dfl.tree_attn_error()
+    a = Append([4, 4], [10, 20], e4m3=e4m3)
+    a.call()
+    assert dfl.tree_attn_error() == 0
+    a.lens[1] = 3
+    a.call()
+    a.table[0][0] = 10 ** 6
+    a.call()
+    assert dfl.tree_attn_error(clear=False) == B.DEVERR_SEQ_LEN | B.DEVERR_PAGE_ID
+    assert dfl.tree_attn_error() == B.DEVERR_SEQ_LEN | B.DEVERR_PAGE_ID and dfl.tree_attn_error() == 0
+    # another stream's are its own
+    s = torch.cuda.Stream()
+    a.call(stream=s)
+    assert dfl.tree_attn_error() == 0 and dfl.tree_attn_error(stream=s) != 0
+    # a given word takes them in place of the library's
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a.call(device_error=word)
+    assert word.item() != 0 and dfl.tree_attn_error() == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_errors_of_a_captured_append(e4m3):
+    a = Append([4, 4], [10, 20], e4m3=e4m3)
+    table, lens, starts = torch.from_numpy(a.table).cuda(), ints(a.lens), ints(a.starts)
+    kw = dict(starts=starts, k_scale=a.scales[0], v_scale=a.scales[1]) if e4m3 else dict(starts=starts)
+    dfl.append_kv(a.k, a.v, *a.caches, table, lens, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dfl.append_kv(a.k, a.v, *a.caches, table, lens, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert dfl.tree_attn_error() == 0
+    lens[1] = 3
+    graph.replay()
+    torch.cuda.synchronize()
+    assert dfl.tree_attn_error() == B.DEVERR_SEQ_LEN and dfl.tree_attn_error() == 0

@@ -1117,7 +1117,12 @@ def rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, inverse: bool = F
          stream=None) -> torch.Tensor:
     """Rotary positions (dflash_rope): x [N, H, D] bf16/fp32 (last dim contiguous, any other strides), positions int32 [N].
     Returns out of x's shape and dtype (a new contiguous tensor, out, or x itself when out is x). inverse turns back,
-    which takes the gradient of the result to the gradient of x."""
+    which takes the gradient of the result to the gradient of x; autograd records a call without an out, and one of an x
+    that requires a gradient is refused with it."""
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("x requires a gradient: a call with an out is not recorded by autograd")
+        return _Turn.apply(x, positions, rope, bool(inverse), stream)
     lib = _lib or load_library()
     shape = x.shape
     if len(shape) != 3 or not x.is_cuda:
@@ -1149,6 +1154,23 @@ def rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, inverse: bool = F
     if st:
         _check(st)
     return out
+
+
+class _Turn(torch.autograd.Function):
+    """rope as autograd records it: the map is linear, and its transpose is the turn back."""
+
+    @staticmethod
+    def forward(ctx, x, positions, turns, inverse, stream):
+        ctx.save_for_backward(positions)
+        ctx.turns, ctx.inverse = turns, inverse
+        return rope(x, positions, turns, inverse=inverse, stream=stream)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (positions,) = ctx.saved_tensors
+        if grad.dim() == 3 and grad.shape[2] > 1 and grad.stride(2) != 1:  # (that of a sum is one number, repeated)
+            grad = grad.contiguous()
+        return rope(grad, positions, ctx.turns, inverse=not ctx.inverse), None, None, None, None
 
 
 _E4M3 = torch.float8_e4m3fn

@@ -638,7 +638,7 @@ typedef struct dflash_rope_freqs {
  *   x, out     device, dtype (bf16 or fp32), element (n, h, d) at n * stride_token + h * stride_head + d; aligned to
  *              the element size (16-byte aligned rows, head_dim a multiple of 16 and rotary_dim one of 16 are read
  *              and written 16 bytes at a time). out is x (same strides: in place) or does not overlap it; its
- *              strides are >= head_dim, x's >= 0.
+ *              strides are >= head_dim, the larger one beyond the rows at the smaller one; x's are >= 0.
  *   positions  device int32 [num_tokens]; any value, negative ones turn backwards.
  * Limits: 0 <= num_tokens <= 2^24 (0 is a no-op), 1 <= num_heads <= 1024, 2 <= head_dim <= DFLASH_MAX_HEAD_DIM.
  * Invalid arguments are reported before any launch. Asynchronous on `stream`; needs no workspace.

@@ -119,7 +119,12 @@ dflash_status dflash_rope(const void* x, void* out, dflash_dtype dtype, int32_t 
     if (num_tokens == 0) return DFLASH_OK;
     if (const dflash_status s = check_rows("x", x, x_stride_token, x_stride_head, dtype)) return s;
     if (const dflash_status s = check_rows("out", out, out_stride_token, out_stride_head, dtype)) return s;
-    if ((num_heads > 1 && out_stride_head < head_dim) || (num_tokens > 1 && out_stride_token < head_dim))
+    // the rows one behind the other at the smaller stride, and those at the larger behind them
+    const bool heads_inside = out_stride_head <= out_stride_token;
+    const int64_t near = heads_inside ? out_stride_head : out_stride_token, far = heads_inside ? out_stride_token : out_stride_head;
+    const int64_t near_n = heads_inside ? num_heads : num_tokens;
+    if ((num_heads > 1 && out_stride_head < head_dim) || (num_tokens > 1 && out_stride_token < head_dim) ||
+        (num_heads > 1 && num_tokens > 1 && far < (near_n - 1) * near + head_dim))
         return report_error(DFLASH_ERR_INVALID_ARG, "the strides of out (%lld, %lld) let its rows overlap",
                             (long long)out_stride_token, (long long)out_stride_head);
     if (!positions || !aligned(positions, 4))

@@ -704,9 +704,10 @@ DFLASH_API dflash_status dflash_append_kv(const void* k, const void* v, int32_t 
  *                 finite, or a score that is not, makes the row NaN with a NaN lse; other rows are not touched by it.
  *   k_cache, v_cache  device, e4m3 bytes, the layout of dflash_block_attn (strides in bytes, multiples of 16). Keys
  *                 outside [first visible, L_b) are never used, whatever they hold. The visible keys' K and V are finite.
- *   k_scale, v_scale  device float32 [num_pages, num_kv_heads], finite and >= 0. The tensor cores take a v_scale of up to
- *                 2^-126 (a page of zeros) as 2^-40. Where a visible page has another outside [2^-40, 2^24], that part of
- *                 the request is worked out on the CUDA cores, at a small fraction of the speed.
+ *   k_scale, v_scale  device float32 [num_pages, num_kv_heads], finite and >= 0. The tensor cores may take a v_scale of up
+ *                 to 2^-126 (a page of zeros) as one of up to 2^-40. Where visible pages have others that lie far apart (outside
+ *                 [2^-40, 2^24] times 1, or times that of the first ones), those parts of the requests are worked out on
+ *                 the CUDA cores, exactly and at a small fraction of the speed.
  *   num_queries, parents  device int32 [B], [B, T], or NULL.
  *   causal        0 or 1; window 0 or W >= 1, in a non-causal block W >= T.
  *   kernel        as in dflash_tree_attn; TC takes bf16 q.

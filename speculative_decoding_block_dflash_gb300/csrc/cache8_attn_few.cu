@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tid < live) {
                 const float tot = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
                 const float lse = tree_row_lse((sm.m[tid] - kLift + log2f(tot)) * kLn2, tot, whole);
-                sm.inv[tid] = tree_inv_sum(tot, whole);
+                sm.inv[tid] = tree_inv_sum(tot, whole) * ms.v_ref;
                 if (!whole)
                     p.part_lse[prow + tid] = lse;
                 else if (p.lse)
@@ -452,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             named_bar_sync_256();  // O, the sums and the masks are read before the next piece's steps
         });
-        if (named_bar_or_256(ok && ms.far != 0)) far_pieces(p, x.page_magic, range, sub, ms.par, lo_s, anc_s);
+        tc_fence_before();
+        asm volatile("barrier.sync 0;" ::: "memory");  // every role is done (the end of the others' branch)
+        if (ms.far != 0) far_pieces(p, x.page_magic, range, sub, ms.v_ref, ms.par, lo_s, anc_s);
     } else {
         give_registers();
         if (warp == kKWarp) {
@@ -559,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
+        // ---------------------------------------------------------------------- teardown
+        tc_fence_before();
+        asm volatile("barrier.sync 0;" ::: "memory");
     }
-    // ---------------------------------------------------------------------- teardown
-    tc_fence_before();
-    __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync_256();
             tc_fence_after();
             const float tot = sm.l[0][row] + sm.l[1][row];
-            const float inv = tree_inv_sum(tot, whole);
+            const float inv = tree_inv_sum(tot, whole) * ms.v_ref;
             if (live_row && half == 0) {
                 const float lse = tree_row_lse((m2 - kLift + log2f(tot)) * kLn2, tot, whole);
                 if (!whole)
@@ -328,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             named_bar_sync_256();  // O, the sums and the masks are read before the next piece's steps
         });
-        if (named_bar_or_256(ok && ms.far != 0)) far_pieces(p, x.page_magic, range, sub, ms.par, lo_s, anc_s);
+        tc_fence_before();
+        asm volatile("barrier.sync 0;" ::: "memory");  // every role is done (the end of the others' branch)
+        if (ms.far != 0) far_pieces(p, x.page_magic, range, sub, ms.v_ref, ms.par, lo_s, anc_s);
     } else {
         give_registers();
         if (warp == kKWarp) {
@@ -433,10 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
+        // ---------------------------------------------------------------------- teardown
+        tc_fence_before();
+        asm volatile("barrier.sync 0;" ::: "memory");
     }
-    // ---------------------------------------------------------------------- teardown
-    tc_fence_before();
-    __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

@@ -18,11 +18,12 @@
 // so that P' is rounded relative to the largest p vs of its row, whatever the scales are; the row sum adds P' / vs in fp32.
 //
 // P' is 0 below 2^-126, and then so is P' / vs, where its key's weight need not be small. So that holds for scales within
-// [2^-40, 2^24], among which no weight above 2^-62 of its row's largest is lost. Scales up to 2^-126, those of pages of zeros,
-// count as 2^-40. A piece with any other scale is worked out once more on the CUDA cores when the CTA is done with all of its
+// [2^-40, 2^24] times a reference, 1 or what the CTA's first tile has, among which no weight above 2^-62 of its row's largest is
+// lost; vs is relative to the reference, and the output is multiplied by it. Scales up to 2^-126, those of pages of zeros, count as
+// 2^-40 of it. A piece with any other scale is worked out once more on the CUDA cores when the CTA is done with all of its
 // pieces, from q, K and V as they are (far_pieces): the loops above know nothing of it. (A second sum of weights in them, which some
 // five forms of cost chunks of 256 queries 3 to 14 % and blocks with a window 2 to 11 % without ever being formed: their code is
-// fetched every time, and their registers are all in use. This costs at most 0.6 us.)
+// fetched every time, and their registers are all in use. This way the measured cases keep their times to 0.3 %.)
 #pragma once
 
 #include <cuda.h>
@@ -47,6 +48,7 @@ constexpr int kStageBytes = 16384;
 constexpr int kMaxStages = 8;  // of each ring
 constexpr int kScaleRing = 8;  // tiles
 constexpr float kNearLow = -40.f, kNearHigh = 24.f;  // logarithms of the value scales that P' and the row sums take
+constexpr float kZeros = 0x1p-126f;                  // value scales up to this are those of pages of zeros
 constexpr int kConverters = 4;
 // warps behind the 8 of the softmax
 constexpr int kKWarp = 8;
@@ -98,7 +100,8 @@ struct Pipe {
     int32_t par[DFLASH_MAX_TREE_NODES];
     int32_t pieces, more;
     Piece piece[kPieces];
-    int32_t far;  // a piece had a value scale too far from 1
+    int32_t far;  // a piece had a value scale too far from the CTA's reference
+    float v_ref;  // that, a power of two
 };
 
 // Bounded wait, of little code: false when it ran out (recorded) or another warp has given up. The test suspends the warp, so
@@ -237,11 +240,16 @@ __device__ __forceinline__ int32_t page_id(const TreeAttnParams& p, const Shape&
     return __ldg(p.page_table + (int64_t)b * p.max_pages + pg);
 }
 
-// Whether a value scale is one that P' does not take.
-__device__ __forceinline__ bool is_far(float v_scale)
-{
-    return v_scale > 0x1p-126f && !(v_scale >= 0x1p-40f && v_scale <= 0x1p24f);
-}
+// The value scales that P' takes beside a reference: those of pages of zeros, and [low, high].
+struct Near {
+    float zeros, low, high;
+    __device__ __forceinline__ explicit Near(float ref)
+        : zeros(ref > 1.f ? -0.5f : kZeros), low(ref * exp2f(kNearLow)), high(ref * exp2f(kNearHigh))
+    {
+        // (beside a reference above 1 a page of zeros would no longer be next to nothing)
+    }
+    __device__ __forceinline__ bool lacks(float scale) const { return scale > zeros && !(scale >= low && scale <= high); }
+};
 
 // A producer warp: K or V by TMA. Boxes without a visible key are fetched at an out-of-bounds page, which the TMA unit fills
 // with zeros. Page ids are asked for a tile ahead. `wait`: a warp's bounded wait.
@@ -312,6 +320,14 @@ __device__ __forceinline__ void produce(const TreeAttnParams& p, const Shape& x,
     __syncwarp();
 }
 
+// What a CTA's value scales are relative to: 1 where its first tile's largest one is ordinary, else the power of two below that (a
+// whole warp, a scale a lane). Its logarithm.
+__device__ __forceinline__ int32_t reference(float v_scale)
+{
+    const int32_t none = -1000, top = __reduce_max_sync(0xffffffffu, v_scale > kZeros ? __float2int_rd(log2f(v_scale)) : none);
+    return top == none || (top >= -24 && top <= 16) ? 0 : min(max(top, -70), 100);
+}
+
 // The scale warp: the scales of a tile's groups of keys, a lane each; ids two tiles ahead and scales one.
 template <typename Wait>
 __device__ __forceinline__ void fetch_scales(const TreeAttnParams& p, const Shape& x, PieceWalk& w, int32_t node0, Pipe& ms,
@@ -319,7 +335,9 @@ __device__ __forceinline__ void fetch_scales(const TreeAttnParams& p, const Shap
 {
     const int lane = threadIdx.x & 31;
     RingPos pos{0, 0u};
-    bool ok = true;
+    bool ok = true, first = true;
+    float ref = 0.f;
+    Near near(1.f);
     each_piece(p, w, node0, ms, true, [&](const Piece& pc) {
         const int32_t n = pc.tiles;
         auto group_page = [&](int32_t t) -> int32_t {
@@ -329,7 +347,7 @@ __device__ __forceinline__ void fetch_scales(const TreeAttnParams& p, const Shap
             return page_id(p, x, pc.b, key, slot);
         };
         auto scales_of = [&](int32_t page, float& ks, float& vs) {
-            ks = vs = 1.f;  // keys that nobody sees, or zeros
+            ks = 1.f, vs = -1.f;  // keys that nobody sees, or zeros
             if (page < 0 || page >= p.num_pages) return;
             const int64_t at = (int64_t)page * p.Hkv + pc.g;
             ks = __ldg(p.k_scale + at);
@@ -338,13 +356,20 @@ __device__ __forceinline__ void fetch_scales(const TreeAttnParams& p, const Shap
         float ks, vs;
         scales_of(group_page(0), ks, vs);
         int32_t next_page = group_page(1);
+        if (first) {
+            first = false;
+            const int32_t e = reference(vs);
+            ref = (float)e;
+            near = Near(power_of_two(e));
+            if (lane == 0) ms.v_ref = power_of_two(e);
+        }
 #pragma unroll 1
         for (int32_t t = 0; t < n && ok; ++t) {
             float next_ks, next_vs;
             scales_of(next_page, next_ks, next_vs);
             next_page = group_page(t + 2);
-            if (is_far(vs)) ms.far = 1;
-            const float v_log = fminf(fmaxf(log2f(vs), kNearLow), kNearHigh);
+            if (near.lacks(vs)) ms.far = 1;
+            const float v_log = fminf(fmaxf(log2f(vs) - ref, kNearLow), kNearHigh);  // (kNearLow for vs < 0)
             ok = wait(ms.sc_free + pos.idx, pos.phase ^ 1u);
             if (!ok) break;
             if (lane < kGroups) {
@@ -537,13 +562,14 @@ __device__ __forceinline__ void convert(const TreeAttnParams& p, const Shape& x,
 // there: a warp per row, 8 keys a step, a running maximum of the scores and the sum of the weights beside it. Called by the 8
 // warps of the softmax when all pieces are done; each walks them by itself, as another role may still look at the table.
 static __device__ __noinline__ void far_pieces(const TreeAttnParams& p, uint32_t page_magic, int32_t range, int32_t sub,
-                                               int32_t* par_s, int32_t* lo_s, uint32_t* anc_s)
+                                               float ref, int32_t* par_s, int32_t* lo_s, uint32_t* anc_s)
 {
     constexpr int kWords = DFLASH_MAX_HEAD_DIM / 128;  // of four dims, a lane's
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SubTile st = sub_tile(p, sub);
     const int32_t node0 = st.rt * p.npt, words = (p.T + 31) / 32;
     const float scale = p.scale * kLog2e;
+    const Near near(ref);
     Shape x{};
     x.page_magic = page_magic;
     PieceWalk w;
@@ -560,7 +586,7 @@ static __device__ __noinline__ void far_pieces(const TreeAttnParams& p, uint32_t
             if (key + kGroup <= req.lo) continue;
             int32_t slot;
             const int32_t page = page_id(p, x, w.b, key, slot);
-            if (page >= 0 && page < p.num_pages) far |= is_far(__ldg(p.v_scale + (int64_t)page * p.Hkv + w.g));
+            if (page >= 0 && page < p.num_pages) far |= near.lacks(__ldg(p.v_scale + (int64_t)page * p.Hkv + w.g));
         }
         if (!__any_sync(0xffffffffu, far)) continue;  // (the same for all warps)
         named_bar_sync_256();

@@ -63,7 +63,8 @@ def values_of(t, b, col, scale):
 
 
 SHAPES = [(2, 4, 2, 128), (1, 16, 2, 64), (9, 8, 1, 512), (5, 4, 2, 256), (40, 4, 2, 128), (33, 4, 1, 64), (20, 8, 2, 256)]
-FAR = [(-70, 70), (-126, 40), (-126, 50), (0, 100), (-126, 118), (-64, 0), (-40, 24), (-41, 23), (-125, -60), (60, 60)]
+FAR = [(-70, 70), (-126, 40), (-126, 50), (0, 100), (-126, 118), (-64, 0), (-40, 24), (-41, 23), (-125, -60), (60, 60), (-60, -60), (-90, -65),
+       (80, 95), (-126, 60)]
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
@@ -132,6 +133,9 @@ def test_split_requests_and_many_pieces(T, hq, hkv, d, kernel):
     nb = 240 if T == 1 else 120
     lens = [T + (37 * b) % 400 for b in range(nb)]
     t = Attn([T] * nb, lens, T=T, hq=hq, hkv=hkv, d=d, seed=3)
+    for b in range(1, nb, 3):  # one scale throughout, far from the others'
+        for col in range(-(-lens[b] // t.page)):
+            values_of(t, b, col, 2.0 ** (-50 if b % 2 else 70))
     for b in range(0, nb, 3):
         for col in range(-(-lens[b] // t.page)):
             values_of(t, b, col, 2.0 ** (60 if (col + b) % 4 == 0 else -60))

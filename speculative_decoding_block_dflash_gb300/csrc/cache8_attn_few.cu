@@ -59,25 +59,6 @@ struct FewMisc {
     // then lo [npt], masks of the request's own keys [npt][(T + 31) / 32]
 };
 
-// 8 columns of 32 values, one a lane -> in lanes l, l + 8, ... the maximum (sum) of column l.
-template <bool kSum>
-__device__ __forceinline__ float transpose8(float (&v)[8], int lane)
-{
-    auto join = [](float a, float b) { return kSum ? a + b : fmaxf(a, b); };
-#pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) {
-        const bool upper = (lane & off) != 0;
-#pragma unroll
-        for (int i = 0; i < off; ++i) {
-            const float send = upper ? v[i] : v[i + off];
-            const float keep = upper ? v[i + off] : v[i];
-            v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, off));
-        }
-    }
-    v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 8));
-    return join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
-}
-
 __device__ __forceinline__ void load_row8(const float* src, float (&v)[8])
 {
     const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);

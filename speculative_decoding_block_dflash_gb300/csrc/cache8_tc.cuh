@@ -23,7 +23,7 @@
 // 2^-40 of it. A piece with any other scale is worked out once more on the CUDA cores when the CTA is done with all of its
 // pieces, from q, K and V as they are (far_pieces): the loops above know nothing of it. (A second sum of weights in them, which some
 // five forms of cost chunks of 256 queries 3 to 14 % and blocks with a window 2 to 11 % without ever being formed: their code is
-// fetched every time, and their registers are all in use. This way the measured cases keep their times to 0.3 %.)
+// fetched every time, and their registers are all in use. This way it is 2 % of the latter, 0.6 us, and nothing elsewhere.)
 #pragma once
 
 #include <cuda.h>
@@ -47,7 +47,7 @@ constexpr int kGroups = kTile / kGroup;
 constexpr int kStageBytes = 16384;
 constexpr int kMaxStages = 8;  // of each ring
 constexpr int kScaleRing = 8;  // tiles
-constexpr float kNearLow = -40.f, kNearHigh = 24.f;  // logarithms of the value scales that P' and the row sums take
+constexpr float kNearLow = -40.f, kNearHigh = 24.f;  // logarithms of the value scales that P' and the row sums take (Near)
 constexpr float kZeros = 0x1p-126f;                  // value scales up to this are those of pages of zeros
 constexpr int kConverters = 4;
 // warps behind the 8 of the softmax
@@ -192,6 +192,25 @@ __device__ __forceinline__ void init_pipe(Pipe& ms, int r_empty_count, int p_hal
     ms.abort = 0;
     ms.far = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// 8 columns of 32 values, one a lane -> in lanes l, l + 8, ... the maximum (sum) of column l.
+template <bool kSum>
+__device__ __forceinline__ float transpose8(float (&v)[8], int lane)
+{
+    auto join = [](float a, float b) { return kSum ? a + b : fmaxf(a, b); };
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float send = upper ? v[i] : v[i + off];
+            const float keep = upper ? v[i + off] : v[i];
+            v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, off));
+        }
+    }
+    v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 8));
+    return join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
 // Fills the table with the walk's next pieces (a whole warp; the others wait).
@@ -558,17 +577,150 @@ __device__ __forceinline__ void convert(const TreeAttnParams& p, const Shape& x,
     });
 }
 
-// The pieces of a range with a value scale that is far from 1, on the CUDA cores in fp32, in place of what the tensor cores have left
-// there: a warp per row, 8 keys a step, a running maximum of the scores and the sum of the weights beside it. Called by the 8
-// warps of the softmax when all pieces are done; each walks them by itself, as another role may still look at the table.
-static __device__ __noinline__ void far_pieces(const TreeAttnParams& p, uint32_t page_magic, int32_t range, int32_t sub,
+// Rows [row0, row0 + R) of a piece on the CUDA cores in fp32, 8 keys a step: a warp's lanes share the dims (kWords words of four), and the
+// keys of a step once the dots are added up. m is a row's running maximum, l a lane's part of its sum.
+template <int kWords, int R>
+__device__ __forceinline__ void far_rows(const TreeAttnParams& p, const Shape& x, const TreeReq& req, int32_t b, int32_t g, int32_t first,
+                                         int32_t end, bool whole, int32_t head0, int32_t node0, int32_t row0, int32_t live,
+                                         int64_t prow, const int32_t* lo_s, const uint32_t* anc_s)
+{
+    const int lane = threadIdx.x & 31, words = (p.T + 31) / 32;
+    const float scale = p.scale * kLog2e;
+    auto out_row = [&](int32_t row) -> int64_t {
+        const int32_t nd = row / p.Gc;
+        return ((int64_t)b * p.T + node0 + nd) * p.Hq + head0 + (row - nd * p.Gc);
+    };
+    float q[R][kWords][4], acc[R][kWords][4], m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t orow = out_row(min(row0 + r, live - 1));  // (rows behind the last repeat it and are not written)
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kWords; ++c) {
+            const int32_t d = c * 128 + lane * 4;
+            const uint2 v = d < p.D ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + orow * p.D + d))
+                                    : make_uint2(0, 0);
+            q[r][c][0] = u2f(v.x << 16), q[r][c][1] = u2f(v.x & 0xFFFF0000u);
+            q[r][c][2] = u2f(v.y << 16), q[r][c][3] = u2f(v.y & 0xFFFF0000u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[r][c][u] = 0.f;
+        }
+    }
+#pragma unroll 1
+    for (int32_t key0 = first; key0 < end; key0 += kGroup) {
+        if (key0 + kGroup <= req.lo) continue;
+        int32_t slot;
+        const int32_t page = page_id(p, x, b, key0, slot);
+        const bool good = page >= 0 && page < p.num_pages;  // (else its keys read as zeros, and the error is raised)
+        const int64_t scale_at = (int64_t)page * p.Hkv + g;
+        const float ks = good ? __ldg(p.k_scale + scale_at) : 0.f, vs = good ? __ldg(p.v_scale + scale_at) : 0.f;
+        const int64_t at = (int64_t)page * p.sp + (int64_t)slot * p.ss + (int64_t)g * p.sh;
+        auto load = [&](const void* base, uint32_t (&w)[kGroup][kWords]) {
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+                for (int c = 0; c < kWords; ++c) {
+                    const int32_t d = c * 128 + lane * 4, key = key0 + k;
+                    w[k][c] = 0u;  // (keys that nobody sees may hold anything)
+                    if (good && key >= req.lo && key < end && d < p.D)
+                        w[k][c] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + at + k * p.ss + d));
+                }
+        };
+        uint32_t kw[kGroup][kWords], vw[kGroup][kWords];
+        load(p.k, kw);
+        if (kWords < 4) load(p.v, vw);  // (on its way; registers for a wide head's do not reach)
+        float dot[R][8];
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) {
+            float f[kWords][4];
+#pragma unroll
+            for (int c = 0; c < kWords; ++c) e4m3_values(kw[k][c], f[c]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                dot[r][k] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kWords; ++c)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) dot[r][k] = fmaf(q[r][c][u], f[c][u] * ks, dot[r][k]);
+            }
+        }
+        if (kWords == 4) load(p.v, vw);
+        float weight[R];  // of key `lane & 7`, times its value scale
+        const int32_t key = key0 + (lane & 7), a = key - req.ctx;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int32_t nd = min(row0 + r, live - 1) / p.Gc;
+            const bool on = key < end && (a < 0 ? key >= lo_s[nd] : ((anc_s[nd * words + (a >> 5)] >> (a & 31)) & 1u) != 0);
+            float y = transpose8<true>(dot[r], lane) * scale;
+            y = on ? y : -INFINITY;
+            float top = y;
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            if (top > m[r]) {  // (the same for the whole warp)
+                const float alpha = ex2(m[r] - top);  // 0 from -inf
+                m[r] = top;
+                l[r] *= alpha;
+#pragma unroll
+                for (int c = 0; c < kWords; ++c)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[r][c][u] *= alpha;
+            }
+            const float e = on ? ex2(y - m[r]) : 0.f;
+            l[r] += e;
+            weight[r] = e * vs;
+        }
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) {
+            float f[kWords][4];
+#pragma unroll
+            for (int c = 0; c < kWords; ++c) e4m3_values(vw[k][c], f[c]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float e = __shfl_sync(0xffffffffu, weight[r], k);
+#pragma unroll
+                for (int c = 0; c < kWords; ++c)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[r][c][u] = fmaf(e, f[c][u], acc[r][c][u]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int32_t row = row0 + r;
+        float sum = l[r];
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (row >= live) continue;
+        const int64_t orow = out_row(row);
+        const float inv = tree_inv_sum(sum, whole), lse = tree_row_lse((m[r] + log2f(sum)) * kLn2, sum, whole);
+        if (lane == 0 && !whole) p.part_lse[prow + row] = lse;
+        if (lane == 0 && whole && p.lse) p.lse[orow] = lse;
+#pragma unroll
+        for (int c = 0; c < kWords; ++c) {
+            const int32_t d = c * 128 + lane * 4;
+            if (d >= p.D) continue;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (!whole)
+                    p.part_out[(prow + row) * p.DV + d + u] = acc[r][c][u] * inv;
+                else
+                    static_cast<__nv_bfloat16*>(p.out)[orow * p.D + d + u] = __float2bfloat16_rn(acc[r][c][u] * inv);
+            }
+        }
+    }
+}
+
+// The pieces of a range with a value scale that P' does not take, in place of what the tensor cores have left there. Called by the 8
+// warps of the softmax when every role is done; each walks the range by itself. A warp takes as many rows at once as its registers
+// hold: 256 queries of 2 requests of 8192 keys, 32/8 heads of 128, take 7 ms, 75 ms a row at a time. (As a function that is called it
+// took registers of the loops before it: single tokens on long contexts 193 us in place of 183.)
+__device__ __forceinline__ void far_pieces(const TreeAttnParams& p, uint32_t page_magic, int32_t range, int32_t sub,
                                                float ref, int32_t* par_s, int32_t* lo_s, uint32_t* anc_s)
 {
-    constexpr int kWords = DFLASH_MAX_HEAD_DIM / 128;  // of four dims, a lane's
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SubTile st = sub_tile(p, sub);
-    const int32_t node0 = st.rt * p.npt, words = (p.T + 31) / 32;
-    const float scale = p.scale * kLog2e;
+    const int32_t node0 = st.rt * p.npt;
     const Near near(ref);
     Shape x{};
     x.page_magic = page_magic;
@@ -594,111 +746,19 @@ static __device__ __noinline__ void far_pieces(const TreeAttnParams& p, uint32_t
         named_bar_sync_256();
         tree_walk_nodes(p, req, node0, min(p.npt, req.n - node0), par_s, anc_s, lo_s, tid, 256);
         named_bar_sync_256();
-        const int32_t live = min(p.npt, req.n - node0) * p.Gc;
+        const int32_t live = min(p.npt, req.n - node0) * p.Gc, head0 = w.g * p.G + st.gc * p.Gc;
         const bool whole = w.whole();
         const int64_t prow = tree_part_row(p, range, sub, w.slot());
+        auto rows = [&](auto run, int32_t at_once) {
 #pragma unroll 1
-        for (int32_t row = warp; row < live; row += 8) {
-            const int32_t nd = row / p.Gc;
-            const int64_t orow =
-                ((int64_t)w.b * p.T + node0 + nd) * p.Hq + w.g * p.G + st.gc * p.Gc + (row - nd * p.Gc);
-            const uint32_t* anc = anc_s + nd * words;
-            const int32_t lo = lo_s[nd];
-            float q[kWords][4], acc[kWords][4];
-#pragma unroll
-            for (int c = 0; c < kWords; ++c) {
-                const int32_t d = c * 128 + lane * 4;
-                const uint2 v = d < p.D ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + orow * p.D + d))
-                                        : make_uint2(0, 0);
-                q[c][0] = u2f(v.x << 16), q[c][1] = u2f(v.x & 0xFFFF0000u);
-                q[c][2] = u2f(v.y << 16), q[c][3] = u2f(v.y & 0xFFFF0000u);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[c][u] = 0.f;
-            }
-            float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-            for (int32_t key0 = first; key0 < end; key0 += kGroup) {
-                uint32_t seen = 0;  // the group's keys that the row sees
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    const int32_t key = key0 + k, a = key - req.ctx;
-                    const bool on = key < end && (a < 0 ? key >= lo : ((anc[a >> 5] >> (a & 31)) & 1u) != 0);
-                    seen |= (uint32_t)on << k;
-                }
-                if (!seen) continue;
-                int32_t slot;
-                const int32_t page = page_id(p, x, w.b, key0, slot);
-                const bool good = page >= 0 && page < p.num_pages;  // (else its keys read as zeros, and the error is raised)
-                const int64_t scale_at = (int64_t)page * p.Hkv + w.g;
-                const float ks = good ? __ldg(p.k_scale + scale_at) : 0.f, vs = good ? __ldg(p.v_scale + scale_at) : 0.f;
-                const int64_t at = (int64_t)page * p.sp + (int64_t)slot * p.ss + (int64_t)w.g * p.sh;
-                uint32_t e4[kGroup][kWords];
-                auto load = [&](const void* base) {
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k)
-#pragma unroll
-                        for (int c = 0; c < kWords; ++c) {
-                            const int32_t d = c * 128 + lane * 4;
-                            e4[k][c] = 0u;
-                            if (good && ((seen >> k) & 1u) && d < p.D)
-                                e4[k][c] =
-                                    __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + at + k * p.ss + d));
-                        }
-                };
-                load(p.k);
-                float y[kGroup], top = m;
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    y[k] = 0.f;
-#pragma unroll
-                    for (int c = 0; c < kWords; ++c) {
-                        float f[4];
-                        e4m3_values(e4[k][c], f);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) y[k] = fmaf(q[c][u], f[u] * ks, y[k]);
-                    }
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) y[k] += __shfl_xor_sync(0xffffffffu, y[k], off);
-                    y[k] *= scale;
-                    if ((seen >> k) & 1u) top = fmaxf(top, y[k]);
-                }
-                load(p.v);
-                const float alpha = top > m ? ex2(m - top) : 1.f;  // 0 from -inf
-                m = top;
-                l *= alpha;
-#pragma unroll
-                for (int c = 0; c < kWords; ++c)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[c][u] *= alpha;
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    const float e = (seen >> k) & 1u ? ex2(y[k] - m) : 0.f;
-                    l += e;
-#pragma unroll
-                    for (int c = 0; c < kWords; ++c) {
-                        float f[4];
-                        e4m3_values(e4[k][c], f);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) acc[c][u] = fmaf(e, f[u] * vs, acc[c][u]);
-                    }
-                }
-            }
-            const float inv = tree_inv_sum(l, whole), lse = tree_row_lse((m + log2f(l)) * kLn2, l, whole);
-            if (lane == 0 && !whole) p.part_lse[prow + row] = lse;
-            if (lane == 0 && whole && p.lse) p.lse[orow] = lse;
-#pragma unroll
-            for (int c = 0; c < kWords; ++c) {
-                const int32_t d = c * 128 + lane * 4;
-                if (d >= p.D) continue;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (!whole)
-                        p.part_out[(prow + row) * p.DV + d + u] = acc[c][u] * inv;
-                    else
-                        static_cast<__nv_bfloat16*>(p.out)[orow * p.D + d + u] = __float2bfloat16_rn(acc[c][u] * inv);
-                }
-            }
-        }
+            for (int32_t row = warp * at_once; row < live; row += 8 * at_once) run(row);
+        };
+        if (p.D <= 128)
+            rows([&](int32_t row) { far_rows<1, 4>(p, x, req, w.b, w.g, first, end, whole, head0, node0, row, live, prow, lo_s, anc_s); }, 4);
+        else if (p.D <= 256)
+            rows([&](int32_t row) { far_rows<2, 2>(p, x, req, w.b, w.g, first, end, whole, head0, node0, row, live, prow, lo_s, anc_s); }, 2);
+        else
+            rows([&](int32_t row) { far_rows<4, 1>(p, x, req, w.b, w.g, first, end, whole, head0, node0, row, live, prow, lo_s, anc_s); }, 1);
     }
 }
 

@@ -661,7 +661,9 @@ DFLASH_API dflash_status dflash_rope(const void* x, void* out, dflash_dtype dtyp
  * of that head (infinities count as the largest float); its bytes are e4m3(x / s), rounded to nearest even (infinities
  * to +-448, NaN to NaN). The earlier tokens' bytes are re-encoded when the scale changes, which is exact but in e4m3's
  * subnormals where their scale was a power of two. Slots of the page behind the new tokens keep their bytes and mean
- * nothing until they are appended to.
+ * nothing until they are appended to. dflash_tree_commit does not take these caches, as a page has one scale: the accepted nodes
+ * of a drafted tree are appended once more, from rows that the caller has kept, to the positions behind the context, where they
+ * overwrite the draft.
  *
  *   k, v          device, dims->dtype (bf16 or fp32), element (row, head, d) at row * stride_token + head *
  *                 stride_head + d, strides >= 0; aligned to the element size (16-byte reads as for dflash_rope).
@@ -701,7 +703,8 @@ DFLASH_API dflash_status dflash_append_kv(const void* k, const void* v, int32_t 
  * and a key whose weight is below 2^-62 of its row's largest may be missing from them.
  *
  *   q             device, [B*T, Hq, D] contiguous, dims->dtype; padding rows may hold anything. A row of q that is not
- *                 finite, or a score that is not, makes the row NaN with a NaN lse; other rows are not touched by it.
+ *                 finite, a score of NaN or +inf, or no score above -inf makes the row NaN with a NaN lse; other rows are
+ *                 not touched by it. (One score of -inf among others is a weight of 0.)
  *   k_cache, v_cache  device, e4m3 bytes, the layout of dflash_block_attn (strides in bytes, multiples of 16). Keys
  *                 outside [first visible, L_b) are never used, whatever they hold. The visible keys' K and V are finite.
  *   k_scale, v_scale  device float32 [num_pages, num_kv_heads], finite and >= 0. The tensor cores may take a v_scale of up

@@ -26,7 +26,7 @@ constexpr int kKeep = 4;      // units of a page and head that a lane holds in r
 
 // Where pair i of row c lies in the table: neighbouring units' pairs j are neighbours, and rows are 64 bytes apart modulo a
 // line, so that a warp's reads (pair j of 8 units of 4 rows) meet all banks. (Pairs one behind the other met 4 banks: 31.5 us in
-// place of 29 for 9250 tokens of 8 heads of 128.)
+// place of 29 for 9934 tokens of 8 heads of 128.)
 struct TableAt {
     int32_t units, stride;
     __device__ __forceinline__ explicit TableAt(int32_t half) : units((half + 7) / 8), stride(8 * units + 8) {}

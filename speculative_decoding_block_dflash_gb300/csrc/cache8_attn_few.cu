@@ -7,9 +7,9 @@
 //
 // K and V are operands as they come from the cache, V's stages as MN-major ones, so that a byte of the cache is written to
 // shared memory once and read from it once. Bound: the bytes, where requests are long: one token each of 32 requests of 1k
-// to 32k keys (32/8 heads of 128, 1.11 GB) takes 178 to 197 us, 5.6 to 6.2 TB/s. At that rate an SM takes in 23
+// to 32k keys (32/8 heads of 128, 1.11 GB) takes 183 to 197 us, 5.6 to 6.1 TB/s. At that rate an SM takes in 23
 // bytes a cycle and its shared memory moves 128, of which widening V to 16 bits took 6 a byte (262 us, the MMAs waiting for shared
-// memory). Blocks of 9 queries of 32/4 heads of 512 over 60k to 131k keys of 4 requests (1.57 GB) take 355 to 361 us, 4.4 TB/s: 72
+// memory). Blocks of 9 queries of 32/4 heads of 512 over 60k to 131k keys of 4 requests (1.57 GB) take 346 to 353 us, 4.5 TB/s: 72
 // rows leave rings of 2 stages each, and the softmax of a tile and its MMAs partly wait for each other.
 //
 // P' (cache8_tc.cuh) in three e5m2 numbers: as fp16, whose upper byte an e5m2 number is, P' loses its upper byte twice and

@@ -13,7 +13,7 @@
 // Bound: the chain of one tile. 128 rows x 128 keys x 128 dims take some 2400 cycles, the MMAs 1072 of them and the exponentials
 // 1024; the widening of V takes about as long beside them. Trees of 32 nodes on 8 requests of 2k to 16k keys (32/8
 // heads of 128) take 70 us, 34 GFLOP and 154 MB at 490 TFLOP/s and 2.2 TB/s, chunks of 256 queries of 2 requests of 8k to
-// 16k keys 150 us, 101 GFLOP at 673 TFLOP/s.
+// 16k keys 149 us, 101 GFLOP at 673 TFLOP/s.
 //
 // Every mbarrier wait is bounded (p.wait_ns): on expiry the kernel records DFLASH_DEVERR_TIMEOUT, waits (bounded) for
 // its own copies and MMAs, frees TMEM and returns.

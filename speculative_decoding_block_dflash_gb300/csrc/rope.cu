@@ -7,7 +7,7 @@
 // flight at a time. A unit's 8 angles cost some 300 instructions and are worked out once for the thread's heads: as many of
 // them as leave the GPU a wave of threads, and one where only latency counts. Units of pairs and of plain dims go to
 // warps of their own, so that the copies do not wait for angles. Bound: the bytes, read and written once, in large calls
-// (8191 tokens of 32 heads of 128 in bf16, 134 MB: 27 us, 5.0 TB/s), and the launch in small ones (12 us by the host's clock).
+// (8191 tokens of 32 heads of 128 in bf16, 134 MB: 28.4 us, 4.7 TB/s), and the launch in small ones (12 us by the host's clock).
 #include <algorithm>
 
 #include "rope.cuh"

@@ -123,3 +123,60 @@ def test_errors_of_a_captured_append(e4m3):
     graph.replay()
     torch.cuda.synchronize()
     assert dfl.tree_attn_error() == B.DEVERR_SEQ_LEN and dfl.tree_attn_error() == 0
+
+
+def test_a_drafted_tree_is_committed_by_appending_again():
+    """The accepted nodes' rows, appended once more behind the context, leave what an append of those alone would have: bytes, scales and
+    the next step's attention."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    hkv, d, page, ctx = 2, 64, 16, [21, 40]
+    rope = dfl.make_rope(d)
+    table = torch.arange(12, dtype=torch.int32, device="cuda").flip(0).reshape(2, 6).contiguous()
+    parents = [[-1, 0, 0, 1, 2, 4, 3, 1], [-1, 0, 1, 1, 2, 0, 5, 6]]
+    paths = [[0, 2, 4, 5], [0, 5]]  # the accepted nodes, the bonus token first
+    n = len(parents[0])
+
+    def depth(b, i):
+        return 0 if parents[b][i] < 0 else 1 + depth(b, parents[b][i])
+
+    def rows(count):
+        # magnitudes in [1/4, 4]: never in e4m3's subnormals, so that re-encoding a page loses nothing
+        x = torch.rand((2, count, hkv, d), generator=g, device="cuda") * 3.75 + 0.25
+        return x * (torch.randint(0, 2, x.shape, generator=g, device="cuda") * 2 - 1)
+
+    def caches():
+        c = [torch.zeros((12, page, hkv, d), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+        return c, [torch.zeros((12, hkv), device="cuda") for _ in range(2)]
+
+    def append(where, k, v, starts, lens, positions=None):
+        dfl.append_kv(k, v, *where[0], table, ints(lens), starts=ints(starts), rope=rope, positions=positions, k_scale=where[1][0],
+                      v_scale=where[1][1])
+
+    old = rows(sum(ctx))
+    tree = rows(2 * n)
+    tree[1] *= 8.0  # the draft's values move the pages' scales
+    at = ints([c + depth(b, i) for b, c in enumerate(ctx) for i in range(n)])
+    take = torch.tensor([b * n + i for b in range(2) for i in paths[b]], device="cuda")
+    starts = [0, len(paths[0]), len(paths[0]) + len(paths[1])]
+    lens = [c + len(x) for c, x in zip(ctx, paths)]
+    drafted, plain = caches(), caches()
+    for where in (drafted, plain):
+        append(where, old[0], old[1], [0, ctx[0], sum(ctx)], ctx)
+    append(drafted, tree[0], tree[1], [0, n, 2 * n], [c + n for c in ctx], at)
+    q = torch.randn((2 * n, 4, d), generator=g, device="cuda").to(torch.bfloat16)
+    full = [c + n for c in ctx]
+    out, _ = dfl.cache8_attn(dfl.rope(q, at, rope), *drafted[0], *drafted[1], table, ints(full), n, parents=ints(parents))
+    assert out.isfinite().all()
+    for where in (drafted, plain):
+        append(where, tree[0][take], tree[1][take], starts, lens)  # (a node's depth is its place behind the context)
+    for b, L in enumerate(lens):
+        j = torch.arange(L, device="cuda")
+        pg, sl = table[b][j // page].long(), j % page
+        for c, e in zip(drafted[0], plain[0]):
+            assert torch.equal(c.view(torch.uint8)[pg, sl], e.view(torch.uint8)[pg, sl])
+        for c, e in zip(drafted[1], plain[1]):
+            assert torch.equal(c[pg], e[pg])
+    step = torch.randn((2, 4, d), generator=g, device="cuda").to(torch.bfloat16)
+    got, want = (dfl.cache8_attn(step, *w[0], *w[1], table, ints(lens), 1) for w in (drafted, plain))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert dfl.tree_attn_error() == 0

@@ -652,8 +652,8 @@ DFLASH_API dflash_status dflash_rope(const void* x, void* out, dflash_dtype dtyp
  * Appends new keys and values to the paged cache, the keys rotated on the way. Request b's n_b new rows are rows
  * starts[b] .. starts[b+1] - 1 of k and v (starts == NULL: num_tokens / batch rows each) and go, in order, to positions
  * L_b - n_b .. L_b - 1 with L_b = seq_lens[b] (the new tokens counted). Rows before starts[0] or from starts[batch] on
- * are padding: what they hold does not matter, but all num_tokens rows of k and v must be readable. A row is rotated to its position in the cache, or to positions[row] where given (drafted
- * trees, whose nodes' positions are not their slots).
+ * are padding: what they hold does not matter, but all num_tokens rows of k and v must be readable. A row is rotated to
+ * its position in the cache, or to positions[row] where given (drafted trees, whose nodes' positions are not their slots).
  *
  * Caches of dims->dtype (no scales): the rotated key in fp32, rounded once; values as they are.
  * e4m3 caches (k_scale and v_scale given): element = e4m3 byte * scale[page][head]. After the call the scale of a page
@@ -677,8 +677,9 @@ DFLASH_API dflash_status dflash_rope(const void* x, void* out, dflash_dtype dtyp
  *   dims          as in dflash_block_attn; num_q_heads is checked and not used.
  *   device_error  device uint32 word (bits OR-ed in) or NULL.
  * A request with new rows whose L_b lies outside [n_b, max_seq_len], or whose rows are not all among the num_tokens (starts
- * below 0, rows that end or lie behind them), is left out (DFLASH_DEVERR_SEQ_LEN, as starts that decrease raise); a page id outside [0, num_pages) sets DFLASH_DEVERR_PAGE_ID and its tokens are left out. Pages
- * that take new tokens must belong to one request only and stand in its table once. Limits: 0 <= num_tokens <= 2^24 (0 is
+ * below 0, rows that end or lie behind them), is left out (DFLASH_DEVERR_SEQ_LEN, which starts that decrease raise as well);
+ * a page id outside [0, num_pages) sets DFLASH_DEVERR_PAGE_ID and its tokens are left out. Pages that take new tokens must
+ * belong to one request only and stand in its table once. Limits: 0 <= num_tokens <= 2^24 (0 is
  * a no-op). Invalid arguments are reported before any launch. Asynchronous on `stream`; needs no workspace.
  */
 DFLASH_API dflash_status dflash_append_kv(const void* k, const void* v, int32_t num_tokens, int64_t k_stride_token,

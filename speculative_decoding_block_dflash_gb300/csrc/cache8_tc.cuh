@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cache8.h"
 #include "e4m3.cuh"
@@ -749,16 +750,19 @@ __device__ __forceinline__ void far_pieces(const TreeAttnParams& p, uint32_t pag
         const int32_t live = min(p.npt, req.n - node0) * p.Gc, head0 = w.g * p.G + st.gc * p.Gc;
         const bool whole = w.whole();
         const int64_t prow = tree_part_row(p, range, sub, w.slot());
-        auto rows = [&](auto run, int32_t at_once) {
+        auto rows = [&](auto words, auto at_once) {
+            constexpr int R = decltype(at_once)::value;
 #pragma unroll 1
-            for (int32_t row = warp * at_once; row < live; row += 8 * at_once) run(row);
+            for (int32_t row = warp * R; row < live; row += 8 * R)
+                far_rows<decltype(words)::value, R>(p, x, req, w.b, w.g, first, end, whole, head0, node0, row, live, prow, lo_s,
+                                                    anc_s);
         };
         if (p.D <= 128)
-            rows([&](int32_t row) { far_rows<1, 4>(p, x, req, w.b, w.g, first, end, whole, head0, node0, row, live, prow, lo_s, anc_s); }, 4);
+            rows(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
         else if (p.D <= 256)
-            rows([&](int32_t row) { far_rows<2, 2>(p, x, req, w.b, w.g, first, end, whole, head0, node0, row, live, prow, lo_s, anc_s); }, 2);
+            rows(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
         else
-            rows([&](int32_t row) { far_rows<4, 1>(p, x, req, w.b, w.g, first, end, whole, head0, node0, row, live, prow, lo_s, anc_s); }, 1);
+            rows(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
     }
 }
 
